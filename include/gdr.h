@@ -61,7 +61,9 @@ typedef enum gdr_status {
     GDR_ERR_TIMEOUT = 6      /* a bounded device-side wait gave up */
 } gdr_status;
 
-typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
+/* GDR_E4M3 (8 bits: sign, 4 exponent, 3 mantissa bits, largest value 448) is
+ * a storage type of the paged key/value cache only. */
+typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1, GDR_E4M3 = 2 } gdr_dtype;
 
 /* Opaque CUDA stream (binary-compatible with cudaStream_t). */
 typedef struct CUstream_st *gdr_stream_t;
@@ -412,6 +414,153 @@ gdr_status gdr_attn_decode_workspace_size(const gdr_attn_decode_args *args, size
 
 gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspace,
                                 size_t workspace_bytes, gdr_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The gated full-attention layer over a paged cache, for any number of new
+ * tokens per sequence: prompts, chunks of prompts, drafted tokens, one token.
+ * The layer is that of gdr_attn_decode_step (the full-attention layers of
+ * the hybrid decoder); the pages keep its cache contiguous, and a server of
+ * many sequences needs it in pages.  Three calls share one cache:
+ *
+ *   gdr_kv_append    rotates the new tokens' q and k and writes k and v into
+ *                    their pages, as bf16 or as 8-bit codes with scales
+ *   gdr_attn_paged   the new tokens attend over their sequence's pages
+ *   gdr_kv_gather    reads cached tokens back into packed rows
+ *
+ * Token t of sequence s lies in row t % page_size of page
+ * page_table[s * table_stride + t / page_size]:
+ *
+ *   k, v             [n_pages, H_kv, page_size, d] in kv_dtype, packed, 16-byte
+ *                    aligned
+ *   k_scale, v_scale [n_pages, H_kv, page_size] fp32, for GDR_E4M3 only (NULL
+ *                    for GDR_BF16): row r stands for scale[r] * codes[r][0..d)
+ *   page_table       device int32 [n_seq, table_width], row stride table_stride
+ *                    (0 = table_width); entries past a sequence's last page are
+ *                    not read
+ *   cu_seqlens       device int32 [n_seq + 1], never decreasing, from 0:
+ *                    sequence s owns rows [cu_seqlens[s], cu_seqlens[s+1]) of
+ *                    the call's packed tensors (its new tokens; for
+ *                    gdr_kv_gather the tokens read).  Empty sequences are
+ *                    allowed.  Packed rows from cu_seqlens[n_seq] on belong to
+ *                    no sequence: they are not read and keep what they hold.
+ *   Supported: d = 256; page_size a power of two, 16 .. 1024; n_pages * H_kv *
+ *   page_size < 2^31 rows; n_tok < 2^31 - 128 (else GDR_ERR_UNSUPPORTED).
+ *
+ * Nothing about the lengths is read on the host, so a captured graph may be
+ * replayed with other lengths in the same arrays.  What only the device can
+ * see is checked there: a page outside [0, n_pages), a token past table_width
+ * pages, a negative length.  Such a token is not written (gdr_kv_append) or
+ * leaves its output row unspecified (gdr_kv_gather, and gdr_attn_paged for
+ * every row of its sequence); nothing outside the buffers is read or written,
+ * and the call's status word is set to GDR_ERR_INVALID_ARG.
+ * Two sequences may share pages that neither writes.
+ * ------------------------------------------------------------------------ */
+typedef struct gdr_kv_pages {
+    int32_t n_seq, H_kv, d, page_size;
+    int32_t n_pages, table_width;
+    int32_t kv_dtype;                 /* GDR_BF16 or GDR_E4M3 */
+    int32_t reserved;                 /* 0 */
+    int64_t table_stride;
+    void *k, *v;                      /* written by gdr_kv_append only */
+    float *k_scale, *v_scale;
+    const int32_t *page_table;
+    const int32_t *cu_seqlens;
+} gdr_kv_pages;
+
+/* Append: new token i of sequence s has position t = cache_len[s] + i.
+ *
+ *   k, v       [n_tok, H_kv, d] bf16   row strides k_stride, v_stride
+ *   q, q_out   [n_tok, H_q, d]  bf16   row strides q_stride, q_out_stride: the
+ *              rotated queries, for gdr_attn_paged; both NULL (and H_q 0) to
+ *              rotate none.  q_out may be q (in place).
+ *   cache_len  device int32 [n_seq]: tokens cached before; read, not updated
+ *   rot_dim, rope_theta   as for gdr_attn_decode_step: the first rot_dim dims of
+ *              q and k are turned in pairs (i, i + rot_dim/2) by t * theta^(-2i/rot_dim)
+ *   GDR_BF16:  the rows are stored as bf16.
+ *   GDR_E4M3:  each row of d values x is stored as
+ *                  scale = max(max|x| / 448, 2^-40),  code = e4m3(x / scale)
+ *              (round to nearest even; x is k after its rotation in fp32, or v).
+ *              A row with an infinity or NaN reads back as not finite.
+ *   status     optional device int32, written only on an error (see above).
+ * Each row of the cache is written by one token as long as no page that is
+ * written belongs to two sequences.  n_tok == 0 or n_seq == 0 is a no-op. */
+typedef struct gdr_kv_append_args {
+    gdr_kv_pages pages;
+    int64_t n_tok;
+    int32_t H_q, rot_dim;
+    float rope_theta;
+    int32_t reserved; /* 0 */
+    int64_t q_stride, q_out_stride, k_stride, v_stride;
+    const void *q, *k, *v;
+    void *q_out;
+    const int32_t *cache_len;
+    int32_t *status;
+} gdr_kv_append_args;
+
+gdr_status gdr_kv_append(const gdr_kv_append_args *args, gdr_stream_t stream);
+
+/* Gather: packed row cu_seqlens[s] + i of k_out, v_out receives token
+ * first[s] + i of sequence s (first NULL = all zero).
+ *
+ *   k_out, v_out  [n_tok, H_kv, d] out_dtype, row strides k_out_stride,
+ *                 v_out_stride; either may be NULL to read the other alone
+ *   status        optional device int32, written only on an error (see above). */
+typedef struct gdr_kv_gather_args {
+    gdr_kv_pages pages;
+    int64_t n_tok;
+    int32_t out_dtype; /* gdr_dtype of k_out, v_out: GDR_BF16 or GDR_F32 */
+    int32_t reserved;  /* 0 */
+    int64_t k_out_stride, v_out_stride;
+    void *k_out, *v_out;
+    const int32_t *first; /* device int32 [n_seq] or NULL */
+    int32_t *status;
+} gdr_kv_gather_args;
+
+gdr_status gdr_kv_gather(const gdr_kv_gather_args *args, gdr_stream_t stream);
+
+/* Attention of the new tokens: row i of sequence s, at position
+ * t = cache_len[s] + i, attends tokens 0 .. t of its sequence, its own among
+ * them (append first, then attend).  With kv head g = floor(h * H_kv / H_q):
+ *
+ *     a_j  = scale * q_h . k_g[j],   lse_h = log sum_{j <= t} exp(a_j)
+ *     y_h  = (sum_{j <= t} exp(a_j - lse_h) v_g[j]) * sigmoid(gate_h)
+ *
+ *   q, gate    [n_tok, H_q, d] bf16, row strides q_stride, gate_stride; q as
+ *              gdr_kv_append leaves it (rotated); gate NULL for no gate
+ *   cache_len  device int32 [n_seq]: tokens cached before the new ones
+ *   out        [n_tok, H_q, d] out_dtype, row stride out_stride
+ *   lse        [n_tok, H_q] fp32, row stride lse_stride (0 = H_q), or NULL
+ *   scale      positive and finite (d^-1/2 for standard attention)
+ *   Supported: H_q a multiple of H_kv with H_q / H_kv <= 128.
+ *   Cached rows below a sequence's length must be finite; what pages hold past
+ *   it does not matter.
+ *   n_tok == 0 or n_seq == 0 is a no-op (workspace 0).
+ *   workspace: gdr_attn_paged_workspace_size bytes, 16-byte aligned, free for
+ *   reuse once the queued work has finished; calls that may run at the same time
+ *   need one each.  Its first 4 bytes (int32) hold, once the work has
+ *   finished, 0, GDR_ERR_INVALID_ARG (see above) or GDR_ERR_TIMEOUT (a bounded
+ *   device-side wait gave up; outputs incomplete). */
+typedef struct gdr_attn_paged_args {
+    gdr_kv_pages pages;
+    int64_t n_tok;
+    int32_t H_q;
+    int32_t out_dtype; /* gdr_dtype of out: GDR_BF16 or GDR_F32 */
+    float scale;
+    int32_t reserved;  /* 0 */
+    int64_t q_stride, gate_stride, out_stride, lse_stride;
+    const void *q, *gate;
+    const int32_t *cache_len;
+    void *out;
+    float *lse;
+} gdr_attn_paged_args;
+
+/* Workspace bytes gdr_attn_paged needs for these arguments on the current
+ * device (only sizes are read; it does not depend on the lengths).  Returns the status
+ * gdr_attn_paged's checks of the sizes would. */
+gdr_status gdr_attn_paged_workspace_size(const gdr_attn_paged_args *args, size_t *bytes);
+
+gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace,
+                          size_t workspace_bytes, gdr_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * The routed-expert MoE feed-forward block at decode time (the FFN of the

@@ -11,6 +11,9 @@ kernels.  PyTorch is used for device memory and streams only.
     rmsnorm_gated(o, z, out, ...)                          the output gate alone
     attn_decode_step(q, gate, k, v, k_cache, v_cache, cache_len, out, ...)
                                                            gated full-attention decode
+    kv_append(k, v, k_pages, v_pages, ...)                  new tokens into a paged cache
+    attn_paged(q, k_pages, v_pages, ...)                    new tokens attend over the pages
+    kv_gather(k_pages, v_pages, ...)                        cached tokens read back
     moe_decode(x, w_router, w_gate_up, w_down, out, ...)    routed-expert MoE block
 """
 from __future__ import annotations
@@ -20,11 +23,12 @@ import ctypes
 import torch
 
 from . import _abi
-from ._abi import GDR_BF16, GDR_F32
+from ._abi import GDR_BF16, GDR_E4M3, GDR_F32
 
 __all__ = ["GdrError", "decode_step", "decode_multi", "prefill_chunked", "prefill_chunked_noalloc",
            "prefill_noalloc_status", "prefill_workspace_size", "attn_decode_step",
-           "attn_decode_workspace_size", "moe_decode", "moe_workspace_size",
+           "attn_decode_workspace_size", "kv_append", "kv_gather", "attn_paged",
+           "attn_paged_workspace_size", "moe_decode", "moe_workspace_size",
            "rmsnorm_gated", "version", "status_string"]
 
 
@@ -384,6 +388,219 @@ def attn_decode_step(q, gate, k, v, k_cache, v_cache, cache_len, out, *, kv_boun
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(L.gdr_attn_decode_step(ctypes.byref(a), _ptr(workspace), ws_bytes,
                                   _stream(stream, q.device)), "gdr_attn_decode_step")
+    return out
+
+
+def _distinct_rows(t, what):
+    """_row_stride of a tensor whose rows must not be one row expanded (a stride of 0
+    stands for packed rows in the C ABI)."""
+    s = _row_stride(t, what)
+    if s == 0 and t.shape[0] > 1:
+        raise ValueError(f"{what}: rows are expanded, make it contiguous")
+    return s
+
+
+def _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale):
+    """The paged cache as the library's struct (gdr_kv_pages)."""
+    if k_pages.dtype == torch.bfloat16:
+        code = GDR_BF16
+    elif k_pages.dtype == torch.float8_e4m3fn:
+        code = GDR_E4M3
+    else:
+        raise TypeError(f"k_pages: dtype {k_pages.dtype} is not bf16 or float8_e4m3fn")
+    shape = k_pages.shape
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != k_pages.dtype:
+            raise TypeError("k_pages and v_pages must have one dtype")
+        if t.dim() != 4 or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a packed [n_pages, H_kv, page_size, d] tensor")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if (t is None) != (code == GDR_BF16):
+            raise ValueError(f"{name} is given with float8_e4m3fn pages, and only then")
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape[:3]
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a packed fp32 [n_pages, H_kv, page_size] tensor")
+    if page_table.dtype != torch.int32 or cu_seqlens.dtype != torch.int32:
+        raise TypeError("page_table and cu_seqlens must be int32")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [n_seq, table_width] with packed rows")
+    n_seq = page_table.shape[0]
+    if n_seq > 1 and page_table.stride(0) < page_table.shape[1]:
+        raise ValueError("page_table's rows must not overlap (an expanded table: make it contiguous)")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != n_seq + 1 or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must hold n_seq + 1 entries")
+    return _abi.KvPages(
+        n_seq=n_seq, H_kv=shape[1], d=shape[3], page_size=shape[2], n_pages=shape[0],
+        table_width=page_table.shape[1], kv_dtype=code, reserved=0,
+        table_stride=page_table.stride(0) if n_seq > 1 else 0,
+        k=k_pages.data_ptr(), v=v_pages.data_ptr(), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
+        page_table=page_table.data_ptr(), cu_seqlens=cu_seqlens.data_ptr())
+
+
+def _rows_bf16(t, name, rows, H, d):
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bf16")
+    if t.shape != (rows, H, d):
+        raise ValueError(f"{name} must be [{rows}, {H}, {d}]")
+
+
+def _per_seq(t, name, n_seq):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.dim() != 1 or t.shape[0] != n_seq or not t.is_contiguous():
+        raise ValueError(f"{name} must hold n_seq entries")
+
+
+def _status_word(status):
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise TypeError("status must be int32")
+
+
+def _one_device(t0, *rest):
+    for t in rest:
+        if t is not None and t.device != t0.device:
+            raise ValueError(f"all tensors must be on one device: {t0.device} and {t.device}")
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, cache_len, *, k_scale=None,
+              v_scale=None, q=None, q_out=None, rot_dim=64, rope_theta=1e7, status=None,
+              stream=None):
+    """Write the new tokens of packed sequences into a paged cache (gdr_kv_append).
+
+    k, v [n_tok, H_kv, 256] bf16: sequence s's new tokens are rows
+    cu_seqlens[s] .. cu_seqlens[s+1]-1, at positions cache_len[s] + i; k is rotated
+    (first ``rot_dim`` dims).  k_pages, v_pages [n_pages, H_kv, page_size, 256]: bf16,
+    or float8_e4m3fn with k_scale, v_scale [n_pages, H_kv, page_size] fp32, then each
+    row is stored as codes of x / scale with scale = max|x| / 448.  page_table
+    [n_seq, table_width], cu_seqlens [n_seq + 1], cache_len [n_seq]: int32 on the
+    device; cache_len is not updated.  ``q``, ``q_out`` [n_tok, H_q, 256] bf16: q_out
+    receives q rotated the same way (it may be q).  ``status``: a device int32,
+    written only when a token has no valid page.  Returns q_out.
+    """
+    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
+    n, H_kv, d = k.shape[0], pages.H_kv, pages.d
+    _rows_bf16(k, "k", n, H_kv, d)
+    _rows_bf16(v, "v", n, H_kv, d)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given together")
+    H_q = 0
+    if q is not None:
+        H_q = q.shape[1]
+        _rows_bf16(q, "q", n, H_q, d)
+        _rows_bf16(q_out, "q_out", n, H_q, d)
+    _per_seq(cache_len, "cache_len", pages.n_seq)
+    _status_word(status)
+    _one_device(k, v, k_pages, v_pages, page_table, cu_seqlens, cache_len, k_scale, v_scale, q,
+                q_out, status)
+    a = _abi.KvAppendArgs(
+        pages=pages, n_tok=n, H_q=H_q, rot_dim=int(rot_dim), rope_theta=float(rope_theta),
+        reserved=0, q_stride=_distinct_rows(q, "q") if H_q else 0,
+        q_out_stride=_distinct_rows(q_out, "q_out") if H_q else 0, k_stride=_distinct_rows(k, "k"),
+        v_stride=_distinct_rows(v, "v"), q=_ptr(q), k=_ptr(k), v=_ptr(v), q_out=_ptr(q_out),
+        cache_len=_ptr(cache_len), status=_ptr(status))
+    _check(_abi.lib().gdr_kv_append(ctypes.byref(a), _stream(stream, k.device)), "gdr_kv_append")
+    return q_out
+
+
+def kv_gather(k_pages, v_pages, page_table, cu_seqlens, k_out, v_out, *, k_scale=None,
+              v_scale=None, first=None, status=None, stream=None):
+    """Read cached tokens back into packed rows (gdr_kv_gather).
+
+    Row cu_seqlens[s] + i of k_out, v_out [n_tok, H_kv, 256] (bf16 or fp32; either may
+    be None) receives token first[s] + i of sequence s (``first`` int32 [n_seq] on the
+    device; None: from token 0).  The cache's tensors are those of kv_append.
+    Returns (k_out, v_out).
+    """
+    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        raise ValueError("one of k_out and v_out is needed")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            continue
+        if t.dtype != some.dtype:
+            raise TypeError("k_out and v_out must have one dtype")
+        if t.shape != (some.shape[0], pages.H_kv, pages.d):
+            raise ValueError(f"{name} must be [n_tok, H_kv, d]")
+    if first is not None:
+        _per_seq(first, "first", pages.n_seq)
+    _status_word(status)
+    _one_device(some, v_out, k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale, first,
+                status)
+    a = _abi.KvGatherArgs(
+        pages=pages, n_tok=some.shape[0], out_dtype=_dtype_code(some, "k_out"), reserved=0,
+        k_out_stride=_distinct_rows(k_out, "k_out") if k_out is not None else 0,
+        v_out_stride=_distinct_rows(v_out, "v_out") if v_out is not None else 0,
+        k_out=_ptr(k_out), v_out=_ptr(v_out), first=_ptr(first), status=_ptr(status))
+    _check(_abi.lib().gdr_kv_gather(ctypes.byref(a), _stream(stream, some.device)), "gdr_kv_gather")
+    return k_out, v_out
+
+
+def _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale,
+                     gate, lse, scale):
+    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
+    d = pages.d
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tok, H_q, d]")
+    n, H_q = q.shape[0], q.shape[1]
+    _rows_bf16(q, "q", n, H_q, d)
+    if gate is not None:
+        _rows_bf16(gate, "gate", n, H_q, d)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _f32_tensor(lse, "lse")
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [n_tok, H_q]")
+    _per_seq(cache_len, "cache_len", pages.n_seq)
+    _one_device(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale, gate,
+                lse)
+    return _abi.AttnPagedArgs(
+        pages=pages, n_tok=n, H_q=H_q, out_dtype=_dtype_code(out, "out"),
+        scale=float(d ** -0.5 if scale is None else scale), reserved=0,
+        q_stride=_distinct_rows(q, "q"),
+        gate_stride=_distinct_rows(gate, "gate") if gate is not None else 0,
+        out_stride=_distinct_rows(out, "out"),
+        lse_stride=_distinct_rows(lse, "lse") if lse is not None else 0,
+        q=_ptr(q), gate=_ptr(gate), cache_len=_ptr(cache_len), out=_ptr(out), lse=_ptr(lse))
+
+
+def attn_paged_workspace_size(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *,
+                              k_scale=None, v_scale=None, gate=None, lse=None, scale=None) -> int:
+    a = _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale,
+                         v_scale, gate, lse, scale)
+    n = ctypes.c_size_t(0)
+    _check(_abi.lib().gdr_attn_paged_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+           "gdr_attn_paged_workspace_size")
+    return int(n.value)
+
+
+def attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *, k_scale=None,
+               v_scale=None, gate=None, lse=None, scale=None, workspace=None,
+               stream=None) -> torch.Tensor:
+    """The new tokens of packed sequences attend over their pages (gdr_attn_paged).
+
+    q [n_tok, H_q, 256] bf16, rotated (kv_append's q_out): sequence s's new tokens are
+    rows cu_seqlens[s] .. cu_seqlens[s+1]-1, the last tokens of its cache (append them
+    first); row i attends tokens 0 .. cache_len[s] + i.  ``gate`` [n_tok, H_q, 256] bf16
+    or None: the output is multiplied by sigmoid(gate).  out [n_tok, H_q, 256] bf16 or
+    fp32; ``lse`` [n_tok, H_q] fp32 or None receives the log of the softmax sums.  The
+    cache's tensors are those of kv_append.  ``workspace``: a uint8 device tensor of
+    attn_paged_workspace_size() bytes (about 39 MB, whatever the lengths), allocated
+    here when None; its first 4 bytes (int32) are the call's status word.
+    """
+    a = _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale,
+                         v_scale, gate, lse, scale)
+    L = _abi.lib()
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        _check(L.gdr_attn_paged_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+               "gdr_attn_paged_workspace_size")
+        if n.value:
+            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(L.gdr_attn_paged(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream(stream, q.device)),
+           "gdr_attn_paged")
     return out
 
 

@@ -15,6 +15,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "gdr.h")
 
 GDR_F32 = 0
 GDR_BF16 = 1
+GDR_E4M3 = 2
 GDR_DECODE_OVERLAP_STATE_LOAD = 1
 GDR_GATE_FROM_RAW = 2
 GDR_PREFILL_NOALLOC_MAX_SEQS = 4096
@@ -86,6 +87,42 @@ class AttnDecodeArgs(ctypes.Structure):
     ]
 
 
+class KvPages(ctypes.Structure):
+    _fields_ = [
+        ("n_seq", _i32), ("H_kv", _i32), ("d", _i32), ("page_size", _i32),
+        ("n_pages", _i32), ("table_width", _i32), ("kv_dtype", _i32), ("reserved", _i32),
+        ("table_stride", _i64),
+        ("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp),
+        ("page_table", _vp), ("cu_seqlens", _vp),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("pages", KvPages), ("n_tok", _i64), ("H_q", _i32), ("rot_dim", _i32),
+        ("rope_theta", _f32), ("reserved", _i32),
+        ("q_stride", _i64), ("q_out_stride", _i64), ("k_stride", _i64), ("v_stride", _i64),
+        ("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp), ("cache_len", _vp), ("status", _vp),
+    ]
+
+
+class KvGatherArgs(ctypes.Structure):
+    _fields_ = [
+        ("pages", KvPages), ("n_tok", _i64), ("out_dtype", _i32), ("reserved", _i32),
+        ("k_out_stride", _i64), ("v_out_stride", _i64),
+        ("k_out", _vp), ("v_out", _vp), ("first", _vp), ("status", _vp),
+    ]
+
+
+class AttnPagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("pages", KvPages), ("n_tok", _i64), ("H_q", _i32), ("out_dtype", _i32),
+        ("scale", _f32), ("reserved", _i32),
+        ("q_stride", _i64), ("gate_stride", _i64), ("out_stride", _i64), ("lse_stride", _i64),
+        ("q", _vp), ("gate", _vp), ("cache_len", _vp), ("out", _vp), ("lse", _vp),
+    ]
+
+
 class MoeArgs(ctypes.Structure):
     _fields_ = [
         ("n_tok", _i32), ("hidden", _i32), ("n_exp", _i32), ("top_k", _i32), ("inter", _i32),
@@ -139,6 +176,15 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
     h.gdr_attn_decode_workspace_size.restype = ctypes.c_int
     h.gdr_attn_decode_step.argtypes = [ctypes.POINTER(AttnDecodeArgs), _vp, ctypes.c_size_t, _vp]
     h.gdr_attn_decode_step.restype = ctypes.c_int
+    h.gdr_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _vp]
+    h.gdr_kv_append.restype = ctypes.c_int
+    h.gdr_kv_gather.argtypes = [ctypes.POINTER(KvGatherArgs), _vp]
+    h.gdr_kv_gather.restype = ctypes.c_int
+    h.gdr_attn_paged_workspace_size.argtypes = [ctypes.POINTER(AttnPagedArgs),
+                                                ctypes.POINTER(ctypes.c_size_t)]
+    h.gdr_attn_paged_workspace_size.restype = ctypes.c_int
+    h.gdr_attn_paged.argtypes = [ctypes.POINTER(AttnPagedArgs), _vp, ctypes.c_size_t, _vp]
+    h.gdr_attn_paged.restype = ctypes.c_int
     h.gdr_moe_workspace_size.argtypes = [ctypes.POINTER(MoeArgs), ctypes.POINTER(ctypes.c_size_t)]
     h.gdr_moe_workspace_size.restype = ctypes.c_int
     h.gdr_moe_decode.argtypes = [ctypes.POINTER(MoeArgs), _vp, ctypes.c_size_t, _vp]

@@ -27,6 +27,10 @@ size_t attn_workspace_bytes(int batch, int H_kv, int n_items);
 void attn_plan(int batch, int H_kv, int kv_bound, int n_sm, int *n_split, int *split_tok);
 cudaError_t launch_attn_decode_args(const gdr_attn_decode_args *a, int n_split, int split_tok,
                                     void *workspace, cudaStream_t s);
+cudaError_t launch_kv_append(const gdr_kv_append_args *a, cudaStream_t s);
+cudaError_t launch_kv_gather(const gdr_kv_gather_args *a, cudaStream_t s);
+size_t attn_paged_workspace_bytes(int n_sm);
+cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cudaStream_t s);
 size_t moe_workspace_bytes(int n_tok, int n_exp, int top_k, int inter, int s_inter, int hidden);
 size_t moe_route_smem_bytes(int n_tok, int n_exp, int top_k);
 cudaError_t launch_moe_args(const gdr_moe_args *a, void *workspace, cudaStream_t s);
@@ -455,6 +459,131 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *a, void *workspace,
     r.out_stride = os;
     return from_cuda(gdr::launch_attn_decode_args(&r, n_split, split_tok, workspace,
                                                   (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------- paged cache and its attention
+
+// Shape checks of a paged cache and of a call's packed rows; fills in the table stride.
+static gdr_status pages_check(gdr_kv_pages *g, int64_t n_tok) {
+    if (g->n_seq < 0 || g->H_kv <= 0 || g->d <= 0 || g->page_size <= 0 || g->n_pages < 0 ||
+        g->table_width < 0 || g->reserved != 0 || n_tok < 0)
+        return GDR_ERR_INVALID_ARG;
+    if (g->kv_dtype != GDR_BF16 && g->kv_dtype != GDR_E4M3) return GDR_ERR_INVALID_ARG;
+    if (g->table_stride < 0 || (g->table_stride != 0 && g->table_stride < g->table_width))
+        return GDR_ERR_INVALID_ARG;
+    if (g->table_stride == 0) g->table_stride = g->table_width;
+    if (g->d != 256) return GDR_ERR_UNSUPPORTED;
+    if (g->page_size < 16 || g->page_size > 1024 || (g->page_size & (g->page_size - 1)))
+        return GDR_ERR_UNSUPPORTED;
+    // Cache rows and packed rows are addressed with 32-bit signed coordinates.
+    if (g->H_kv > 0x7fffffff / g->page_size ||
+        (int64_t)g->H_kv * g->page_size * g->n_pages > 0x7fffffffLL)
+        return GDR_ERR_UNSUPPORTED;
+    if (n_tok > 0x7fffffffLL - 128) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+// Pointer checks of a paged cache that a call is about to use.
+static gdr_status pages_pointers(const gdr_kv_pages *g) {
+    if (!g->cu_seqlens) return GDR_ERR_INVALID_ARG;
+    if (g->n_pages > 0 && (!g->k || !g->v)) return GDR_ERR_INVALID_ARG;
+    if (g->table_width > 0 && !g->page_table) return GDR_ERR_INVALID_ARG;
+    if (g->kv_dtype == GDR_E4M3 ? (g->n_pages > 0 && (!g->k_scale || !g->v_scale))
+                                : (g->k_scale || g->v_scale))
+        return GDR_ERR_INVALID_ARG;
+    if (!aligned16(g->k) || !aligned16(g->v)) return GDR_ERR_MISALIGNED;
+    if (!aligned4(g->k_scale) || !aligned4(g->v_scale) || !aligned4(g->page_table) ||
+        !aligned4(g->cu_seqlens))
+        return GDR_ERR_MISALIGNED;
+    return GDR_OK;
+}
+
+static gdr_status attn_paged_check(gdr_attn_paged_args *a) {
+    GDR_TRY(pages_check(&a->pages, a->n_tok));
+    if (a->H_q <= 0 || a->reserved != 0 || !dtype_ok(a->out_dtype)) return GDR_ERR_INVALID_ARG;
+    if (a->H_q % a->pages.H_kv != 0) return GDR_ERR_INVALID_ARG;
+    if (!(a->scale > 0.f) || !(a->scale <= 3.4028235e38f)) return GDR_ERR_INVALID_ARG;
+    if (a->H_q / a->pages.H_kv > 128) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
+extern "C" {
+
+gdr_status gdr_kv_append(const gdr_kv_append_args *args, gdr_stream_t stream) {
+    if (!args) return GDR_ERR_INVALID_ARG;
+    gdr_kv_append_args a = *args;
+    GDR_TRY(pages_check(&a.pages, a.n_tok));
+    if (a.H_q < 0 || a.reserved != 0) return GDR_ERR_INVALID_ARG;
+    if (a.rot_dim < 0 || a.rot_dim > a.pages.d || (a.rot_dim & 1)) return GDR_ERR_INVALID_ARG;
+    if (!(a.rope_theta > 0.f) || !(a.rope_theta <= 3.4028235e38f)) return GDR_ERR_INVALID_ARG;
+    if (!a.q != !a.q_out || (a.H_q > 0 && !a.q && a.n_tok > 0) || (a.H_q == 0 && a.q))
+        return GDR_ERR_INVALID_ARG;
+    const int64_t d = a.pages.d;
+    GDR_TRY(resolve_stride(a.q_stride, a.H_q * d, 2, &a.q_stride));
+    GDR_TRY(resolve_stride(a.q_out_stride, a.H_q * d, 2, &a.q_out_stride));
+    GDR_TRY(resolve_stride(a.k_stride, a.pages.H_kv * d, 2, &a.k_stride));
+    GDR_TRY(resolve_stride(a.v_stride, a.pages.H_kv * d, 2, &a.v_stride));
+    if (a.n_tok == 0 || a.pages.n_seq == 0) return GDR_OK;
+    GDR_TRY(pages_pointers(&a.pages));
+    if (!a.k || !a.v || !a.cache_len) return GDR_ERR_INVALID_ARG;
+    // In place, a row of q_out is the row of q it is computed from.
+    if (a.q && a.q == a.q_out && a.q_stride != a.q_out_stride) return GDR_ERR_INVALID_ARG;
+    const void *p16[] = {a.q, a.q_out, a.k, a.v};
+    for (const void *ptr : p16)
+        if (!aligned16(ptr)) return GDR_ERR_MISALIGNED;
+    if (!aligned4(a.cache_len) || !aligned4(a.status)) return GDR_ERR_MISALIGNED;
+    return from_cuda(gdr::launch_kv_append(&a, (cudaStream_t)stream));
+}
+
+gdr_status gdr_kv_gather(const gdr_kv_gather_args *args, gdr_stream_t stream) {
+    if (!args) return GDR_ERR_INVALID_ARG;
+    gdr_kv_gather_args a = *args;
+    GDR_TRY(pages_check(&a.pages, a.n_tok));
+    if (a.reserved != 0 || !dtype_ok(a.out_dtype)) return GDR_ERR_INVALID_ARG;
+    const int64_t packed = (int64_t)a.pages.H_kv * a.pages.d;
+    const size_t esz = dtype_bytes(a.out_dtype);
+    GDR_TRY(resolve_stride(a.k_out_stride, packed, esz, &a.k_out_stride));
+    GDR_TRY(resolve_stride(a.v_out_stride, packed, esz, &a.v_out_stride));
+    if (a.n_tok == 0 || a.pages.n_seq == 0) return GDR_OK;
+    GDR_TRY(pages_pointers(&a.pages));
+    if (!a.k_out && !a.v_out) return GDR_ERR_INVALID_ARG;
+    if (!aligned16(a.k_out) || !aligned16(a.v_out)) return GDR_ERR_MISALIGNED;
+    if (!aligned4(a.first) || !aligned4(a.status)) return GDR_ERR_MISALIGNED;
+    return from_cuda(gdr::launch_kv_gather(&a, (cudaStream_t)stream));
+}
+
+gdr_status gdr_attn_paged_workspace_size(const gdr_attn_paged_args *args, size_t *bytes) {
+    if (!bytes || !args) return GDR_ERR_INVALID_ARG;
+    gdr_attn_paged_args a = *args;
+    GDR_TRY(attn_paged_check(&a));
+    *bytes = a.n_tok == 0 || a.pages.n_seq == 0 ? 0 : gdr::attn_paged_workspace_bytes(device_sm_count());
+    return GDR_OK;
+}
+
+gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace, size_t ws_bytes,
+                          gdr_stream_t stream) {
+    if (!args) return GDR_ERR_INVALID_ARG;
+    gdr_attn_paged_args a = *args;
+    GDR_TRY(attn_paged_check(&a));
+    const int64_t d = a.pages.d;
+    GDR_TRY(resolve_stride(a.q_stride, a.H_q * d, 2, &a.q_stride));
+    GDR_TRY(resolve_stride(a.gate_stride, a.H_q * d, 2, &a.gate_stride));
+    GDR_TRY(resolve_stride(a.out_stride, a.H_q * d, dtype_bytes(a.out_dtype), &a.out_stride));
+    if (a.lse_stride != 0 && a.lse_stride < a.H_q) return GDR_ERR_INVALID_ARG;
+    if (a.lse_stride == 0) a.lse_stride = a.H_q;
+    if (a.n_tok == 0 || a.pages.n_seq == 0) return GDR_OK;
+    GDR_TRY(pages_pointers(&a.pages));
+    if (!a.q || !a.cache_len || !a.out) return GDR_ERR_INVALID_ARG;
+    const void *p16[] = {a.q, a.gate, a.out};
+    for (const void *ptr : p16)
+        if (!aligned16(ptr)) return GDR_ERR_MISALIGNED;
+    if (!aligned4(a.cache_len) || !aligned4(a.lse)) return GDR_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < gdr::attn_paged_workspace_bytes(device_sm_count()))
+        return GDR_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GDR_ERR_MISALIGNED;
+    return from_cuda(gdr::launch_attn_paged(&a, workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,323 @@
+// gdr_kv.cu -- the paged key/value cache of the gated full-attention layer:
+// writing new tokens (rotary embedding, optional 8-bit codes) and reading
+// cached ones back.
+//
+//   append: k' = RoPE(k, t), q' = RoPE(q, t) at position t = cache_len[s] + i
+//           (pairs (j, j + rot_dim/2), angle t theta^(-2j/rot_dim)); k' and v
+//           go to token t's row, as bf16, or as scale = max(max|x|/448, 2^-40)
+//           and codes e4m3(x / scale)
+//   gather: rows scale * codes (or the bf16 rows) into packed rows
+//
+// Both move every byte once and are bound by memory: a warp takes one row of
+// 256 values, 8 a lane, so that bf16 rows move in 16-byte and codes in 8-byte
+// accesses.  The angles are taken in double, once per token for all its heads.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "gdr.h"
+#include "gdr_common.cuh"
+#include "gdr_paged.cuh"
+
+namespace gdr {
+namespace paged {
+
+// Tokens per block: a prompt's blocks take several so that a block's set-up
+// (sequence search, angles) is shared; a few tokens spread over the SMs.
+constexpr int TOKENS = 4;
+constexpr int WARPS = 8;
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40: rows of zeros keep a usable scale
+
+struct AppendParams {
+    gdr_kv_append_args a;
+    int shift;      // log2(page_size)
+    int tokens;     // per block
+    int rows;       // per token: H_q + 2 H_kv
+    double log2_theta;
+};
+
+// 8 bf16 values of a lane as fp32.
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParams p) {
+    __shared__ float2 turn[TOKENS][D / 2];
+    __shared__ int tok_seq[TOKENS];
+    __shared__ int64_t tok_pos[TOKENS];
+    wait_for_predecessor();
+    release_dependents();
+    const gdr_kv_append_args &a = p.a;
+    const gdr_kv_pages &c = a.pages;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int n = (int)min((int64_t)p.tokens, a.n_tok - t0);
+    if (warp < n) {
+        const int t = (int)(t0 + warp);
+        int s = find_sequence(c.cu_seqlens, c.n_seq, t);
+        int64_t pos = 0;
+        if (s < c.n_seq) {
+            const int i = t - __ldg(c.cu_seqlens + s);
+            const int len = __ldg(a.cache_len + s);
+            pos = (int64_t)len + i;
+            if (i < 0) s = c.n_seq;
+            else if (len < 0) pos = -1;  // no valid page
+        }
+        if (lane == 0) {
+            tok_seq[warp] = s;
+            tok_pos[warp] = pos;
+        }
+    }
+    __syncthreads();
+    const int half = a.rot_dim >> 1;
+    for (int i = threadIdx.x; i < n * half; i += 32 * WARPS) {
+        const int tt = i / half, j = i - tt * half;
+        const double ang = (double)tok_pos[tt] * exp2(-(2.0 * j / a.rot_dim) * p.log2_theta);
+        double sn, cs;
+        sincos(ang, &sn, &cs);
+        turn[tt][j] = make_float2((float)cs, (float)sn);
+    }
+    __syncthreads();
+    // Rows of the block: token by token, its q heads, its k heads, its v heads.
+    const int n_rows = n * p.rows;
+    for (int r = blockIdx.y * WARPS + warp; r < n_rows; r += gridDim.y * WARPS) {
+        const int tt = r / p.rows, h = r - tt * p.rows;
+        const int s = tok_seq[tt];
+        if (s >= c.n_seq) continue;
+        const int64_t t = t0 + tt;
+        const bool is_q = h < a.H_q, is_v = h >= a.H_q + c.H_kv;
+        const int g = is_q ? h : is_v ? h - a.H_q - c.H_kv : h - a.H_q;
+        const __nv_bfloat16 *src =
+            (is_q   ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride
+             : is_v ? static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride
+                    : static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride) +
+            g * D;
+        // Not through the read-only path: q_out may be q.
+        const uint4 raw = *reinterpret_cast<const uint4 *>(src + 8 * lane);
+        float x[8];
+        unpack8(raw, x);
+        if (!is_v && half > 0) {
+            if ((half & 7) == 0) {
+                // Partners sit in another lane, at the same place.
+                const int step = half >> 3;
+                const bool low = lane < step, in = lane < 2 * step;
+                const int from = in ? (low ? lane + step : lane - step) : lane;
+                uint4 o;
+                o.x = __shfl_sync(kFullMask, raw.x, from);
+                o.y = __shfl_sync(kFullMask, raw.y, from);
+                o.z = __shfl_sync(kFullMask, raw.z, from);
+                o.w = __shfl_sync(kFullMask, raw.w, from);
+                if (in) {
+                    float y[8];
+                    unpack8(o, y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 cs = turn[tt][8 * (low ? lane : lane - step) + i];
+                        x[i] = low ? x[i] * cs.x - y[i] * cs.y : x[i] * cs.x + y[i] * cs.y;
+                    }
+                }
+            } else {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = 8 * lane + i;
+                    y[i] = d < a.rot_dim ? __bfloat162float(src[d < half ? d + half : d - half]) : 0.f;
+                }
+                __syncwarp();  // every lane has read the row before one writes it in place
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = 8 * lane + i;
+                    if (d < a.rot_dim) {
+                        const float2 cs = turn[tt][d < half ? d : d - half];
+                        x[i] = d < half ? x[i] * cs.x - y[i] * cs.y : x[i] * cs.x + y[i] * cs.y;
+                    }
+                }
+            }
+        }
+        if (is_q) {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.q_out) + t * a.q_out_stride + g * D;
+            *reinterpret_cast<uint4 *>(dst + 8 * lane) = pack8(x);
+            continue;
+        }
+        const int row = cache_row(c, p.shift, s, g, tok_pos[tt]);
+        if (row < 0) {
+            if (lane == 0 && a.status) *a.status = kBadPage;
+            continue;
+        }
+        void *pages = is_v ? c.v : c.k;
+        if constexpr (!E4M3) {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(pages) + (size_t)row * D;
+            *reinterpret_cast<uint4 *>(dst + 8 * lane) = is_v ? raw : pack8(x);
+        } else {
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            const float scale = fmaxf(__fdiv_rn(top, kE4m3Max), kScaleMin);
+            // x / scale itself, not x times a rounded reciprocal: values half way between
+            // two codes are common (x is bf16), and the quotient decides them.
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 lo = make_float2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
+                const float2 hi = make_float2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
+                w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                       ((uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16);
+            }
+            unsigned char *dst = static_cast<unsigned char *>(pages) + (size_t)row * D;
+            *reinterpret_cast<uint2 *>(dst + 8 * lane) = make_uint2(w[0], w[1]);
+            if (lane == 0) (is_v ? c.v_scale : c.k_scale)[row] = scale;
+        }
+    }
+}
+
+struct GatherParams {
+    gdr_kv_gather_args a;
+    int shift;
+    int tokens;
+    int sides;  // rows per token and kv head: K and V, or one of them
+};
+
+template <bool E4M3, typename TOUT>
+__global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const GatherParams p) {
+    __shared__ int tok_seq[TOKENS];
+    __shared__ int64_t tok_pos[TOKENS];
+    wait_for_predecessor();
+    release_dependents();
+    const gdr_kv_gather_args &a = p.a;
+    const gdr_kv_pages &c = a.pages;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int n = (int)min((int64_t)p.tokens, a.n_tok - t0);
+    if (warp < n) {
+        const int t = (int)(t0 + warp);
+        int s = find_sequence(c.cu_seqlens, c.n_seq, t);
+        int64_t pos = 0;
+        if (s < c.n_seq) {
+            const int i = t - __ldg(c.cu_seqlens + s);
+            const int first = a.first ? __ldg(a.first + s) : 0;
+            pos = first < 0 ? -1 : (int64_t)first + i;
+            if (i < 0) s = c.n_seq;
+        }
+        if (lane == 0) {
+            tok_seq[warp] = s;
+            tok_pos[warp] = pos;
+        }
+    }
+    __syncthreads();
+    const int per_tok = c.H_kv * p.sides, n_rows = n * per_tok;
+    for (int r = blockIdx.y * WARPS + warp; r < n_rows; r += gridDim.y * WARPS) {
+        const int tt = r / per_tok, h = r - tt * per_tok;
+        const int s = tok_seq[tt];
+        if (s >= c.n_seq) continue;
+        const int g = h % c.H_kv;
+        const bool is_v = !a.k_out || h >= c.H_kv;
+        const int row = cache_row(c, p.shift, s, g, tok_pos[tt]);
+        if (row < 0) {
+            if (lane == 0 && a.status) *a.status = kBadPage;
+            continue;
+        }
+        const void *pages = is_v ? c.v : c.k;
+        float x[8];
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if constexpr (E4M3) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
+                static_cast<const unsigned char *>(pages) + (size_t)row * D + 8 * lane));
+            const float scale = __ldg((is_v ? c.v_scale : c.k_scale) + row);
+            const uint32_t ww[2] = {w.x, w.y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)(ww[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h2));
+                x[2 * i] = f.x * scale;
+                x[2 * i + 1] = f.y * scale;
+            }
+        } else {
+            raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) +
+                                                        (size_t)row * D + 8 * lane));
+            unpack8(raw, x);
+        }
+        const int64_t at = (t0 + tt) * (is_v ? a.v_out_stride : a.k_out_stride) + g * D + 8 * lane;
+        TOUT *dst = static_cast<TOUT *>(is_v ? a.v_out : a.k_out) + at;
+        if constexpr (sizeof(TOUT) == 2) {
+            *reinterpret_cast<uint4 *>(dst) = E4M3 ? pack8(x) : raw;
+        } else {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    }
+}
+
+// Launch as a programmatic dependent: the kernel waits for its predecessor
+// before it reads anything, so only the launch overlaps.
+template <typename P>
+static cudaError_t launch(void (*kern)(P), const P &p, dim3 grid, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+// Below this many tokens a block takes one token and its rows are spread over
+// several blocks, a warp each; above, a block takes TOKENS tokens.
+constexpr int64_t kFewTokens = 592;  // 4 blocks for each of 148 SMs
+
+static dim3 grid_for(int64_t n_tok, int rows, int *tokens) {
+    *tokens = n_tok <= kFewTokens ? 1 : TOKENS;
+    const unsigned y = *tokens == 1 ? (unsigned)((rows + WARPS - 1) / WARPS) : 1u;
+    return dim3((unsigned)((n_tok + *tokens - 1) / *tokens), y < 65535u ? y : 65535u);
+}
+
+}  // namespace paged
+
+cudaError_t launch_kv_append(const gdr_kv_append_args *a, cudaStream_t s) {
+    paged::AppendParams p = {};
+    p.a = *a;
+    p.shift = paged::log2_of(a->pages.page_size);
+    p.rows = a->H_q + 2 * a->pages.H_kv;
+    p.log2_theta = log2((double)a->rope_theta);
+    const dim3 grid = paged::grid_for(a->n_tok, p.rows, &p.tokens);
+    return a->pages.kv_dtype == GDR_E4M3 ? paged::launch(paged::kv_append_kernel<true>, p, grid, s)
+                                         : paged::launch(paged::kv_append_kernel<false>, p, grid, s);
+}
+
+cudaError_t launch_kv_gather(const gdr_kv_gather_args *a, cudaStream_t s) {
+    paged::GatherParams p = {};
+    p.a = *a;
+    p.shift = paged::log2_of(a->pages.page_size);
+    p.sides = (a->k_out ? 1 : 0) + (a->v_out ? 1 : 0);
+    const dim3 grid = paged::grid_for(a->n_tok, p.sides * a->pages.H_kv, &p.tokens);
+    const bool codes = a->pages.kv_dtype == GDR_E4M3;
+    if (a->out_dtype == GDR_BF16)
+        return codes ? paged::launch(paged::kv_gather_kernel<true, __nv_bfloat16>, p, grid, s)
+                     : paged::launch(paged::kv_gather_kernel<false, __nv_bfloat16>, p, grid, s);
+    return codes ? paged::launch(paged::kv_gather_kernel<true, float>, p, grid, s)
+                 : paged::launch(paged::kv_gather_kernel<false, float>, p, grid, s);
+}
+
+}  // namespace gdr
