@@ -449,7 +449,7 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspac
  * Nothing about the lengths is read on the host, so a captured graph may be
  * replayed with other lengths in the same arrays.  What only the device can
  * see is checked there: a page outside [0, n_pages), a token past table_width
- * pages, a negative length.  Such a token is not written (gdr_kv_append) or
+ * pages, a negative length, one of 2^31 - 256 tokens or more.  Such a token is not written (gdr_kv_append) or
  * leaves its output row unspecified (gdr_kv_gather, and gdr_attn_paged for
  * every row of its sequence); nothing outside the buffers is read or written,
  * and the call's status word is set to GDR_ERR_INVALID_ARG.
@@ -532,8 +532,9 @@ gdr_status gdr_kv_gather(const gdr_kv_gather_args *args, gdr_stream_t stream);
  *   lse        [n_tok, H_q] fp32, row stride lse_stride (0 = H_q), or NULL
  *   scale      positive and finite (d^-1/2 for standard attention)
  *   Supported: H_q a multiple of H_kv with H_q / H_kv <= 128.
- *   Cached rows below a sequence's length must be finite; what pages hold past
- *   it does not matter.
+ *   q and the cached rows below a sequence's length must be finite, and v_scale
+ *   not negative (less than 2^-40 counts as that); what pages hold past the
+ *   length does not matter.
  *   n_tok == 0 or n_seq == 0 is a no-op (workspace 0).
  *   workspace: gdr_attn_paged_workspace_size bytes, 16-byte aligned, free for
  *   reuse once the queued work has finished; calls that may run at the same time

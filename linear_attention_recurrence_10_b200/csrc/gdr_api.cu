@@ -487,11 +487,9 @@ static gdr_status pages_check(gdr_kv_pages *g, int64_t n_tok) {
 
 // Pointer checks of a paged cache that a call is about to use.
 static gdr_status pages_pointers(const gdr_kv_pages *g) {
-    if (!g->cu_seqlens) return GDR_ERR_INVALID_ARG;
-    if (g->n_pages > 0 && (!g->k || !g->v)) return GDR_ERR_INVALID_ARG;
-    if (g->table_width > 0 && !g->page_table) return GDR_ERR_INVALID_ARG;
-    if (g->kv_dtype == GDR_E4M3 ? (g->n_pages > 0 && (!g->k_scale || !g->v_scale))
-                                : (g->k_scale || g->v_scale))
+    if (g->n_pages < 1 || g->table_width < 1) return GDR_ERR_INVALID_ARG;
+    if (!g->cu_seqlens || !g->k || !g->v || !g->page_table) return GDR_ERR_INVALID_ARG;
+    if (g->kv_dtype == GDR_E4M3 ? (!g->k_scale || !g->v_scale) : (g->k_scale || g->v_scale))
         return GDR_ERR_INVALID_ARG;
     if (!aligned16(g->k) || !aligned16(g->v)) return GDR_ERR_MISALIGNED;
     if (!aligned4(g->k_scale) || !aligned4(g->v_scale) || !aligned4(g->page_table) ||

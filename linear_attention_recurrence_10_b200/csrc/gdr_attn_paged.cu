@@ -4,121 +4,1131 @@
 //
 //   a_j = scale q . k_j,  y = (sum_{j <= t} e^{a_j} v_j) / (sum e^{a_j}) * sigmoid(gate)
 //
-// One warp per (token, query head), 8 of the 256 dims a lane; the keys one
-// after another with the running maximum and sum of the softmax.
-#include <cuda_fp8.h>
+// Two kernels on the caller's stream, each a programmatic dependent of the one
+// before:
+//   attend: one CTA per SM.  A work item is a query tile (128 rows: the group's
+//     query heads of 128 / n_rep tokens, so that a key/value tile is read once
+//     for all of them) over the tiles of 128 keys that its last row attends.
+//     The items of the whole batch, each n_kv tiles long plus a fixed cost,
+//     are laid end to end and every CTA takes an equal stretch, so a prompt's
+//     triangle of tiles, a ragged batch and one long sequence all load the SMs
+//     evenly.  Every CTA derives its stretch from the lengths on the device.
+//     An item that a stretch cuts leaves partial results in the workspace.
+//   combine: joins the partial results of the items that were cut.
+//
+// In a CTA, one warp streams K and V through a ring of shared-memory slots with
+// TMA tensor copies, page by page, into 128-byte-swizzled tiles; one thread
+// issues S = Q K^T (M = 128 rows, N = 128 keys, K = 256) and O += P V (N = 256)
+// on tcgen05 with S (two buffers) and O in tensor memory; eight softmax warps
+// (thread = row, two threads a row, 64 keys each) keep the running maximum and
+// sum, write P over S in tensor memory and rescale O when the maximum has moved
+// far.  S of the next tile is computed while the softmax works on this one.
+//
+// A code cache is multiplied as it is, in e4m3, at twice bf16's rate and with
+// nothing to convert: the other operand is split in two e4m3 parts, x ~ hi + lo,
+// which hold 8 significant bits as bf16 does.  Q (bf16) times a power of two
+// per row splits exactly but for values 2^-17 below the row's largest.  The
+// key scales multiply the scores.  The value scales sv_j enter the
+// weights, w_j = 2^(a_j + log2 sv_j - m), which P holds, with the maximum taken
+// over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Four more warps split
+// Q and prepare the scales.
+//
+// Every wait is bounded (2 s); on expiry a role records GDR_ERR_TIMEOUT, the
+// others run into their own limits, copies and commits in flight are waited
+// for (bounded), tensor memory is freed and the CTA returns.
+#include "gdr_tmap.cuh"
 #include <math.h>
+
+#include <type_traits>
 
 #include "gdr.h"
 #include "gdr_common.cuh"
 #include "gdr_paged.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 namespace paged {
 
-struct AttnParams {
-    gdr_attn_paged_args a;
-    int shift;
-    int *status;
+using namespace gdr::tc;
+
+constexpr int ROWS = 128;  // query rows per item
+constexpr int KEYS = 128;  // keys per tile
+// Cost of starting and finishing an item, in tiles.
+constexpr int ITEM_COST = 2;
+constexpr int SOFTMAX_WARPS = 8;
+constexpr int W_LOAD = 8, W_MMA = 9, W_AUX = 10;  // warps 10 .. 13: code caches only
+constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;
+// Unwinding after an expired wait: arrivals still owed come within microseconds
+// if their operations were issued, never if not.
+constexpr uint64_t kDrainNs = 1000000ull;
+constexpr int kTimeout = GDR_ERR_TIMEOUT;
+
+// Shared memory.  Q tile: 4 boxes of [128 rows][128 bytes]; bf16: box c holds
+// dims 64c ..; split e4m3: boxes 2h, 2h + 1 hold the hi and lo parts of dims 128h ...
+constexpr uint32_t BOX = 16384;
+template <bool E4M3>
+struct Layout {
+    // A tile is two K slots and two V slots.  bf16: K slots are halves of the dims
+    // (2 boxes of [128 keys][64 dims]), V slots halves of the keys (4 boxes of
+    // [64 keys][64 dims]).  e4m3: both are halves of the dims ([128 keys][128 dims]).
+    static constexpr uint32_t SLOT = E4M3 ? BOX : 2 * BOX;
+    static constexpr int NSLOT = E4M3 ? 9 : 5;
+    static constexpr uint32_t S_Q = 0;
+    static constexpr uint32_t S_RING = 4 * BOX;
+    static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;      // [2][2][128] floats
+    static constexpr uint32_t S_SCALE = S_RED + 2048;             // [2][3][128] floats
+    static constexpr uint32_t S_ROWK = S_SCALE + (E4M3 ? 3072 : 0);  // [2][128] floats
+    static constexpr uint32_t S_BAR = S_ROWK + (E4M3 ? 1024 : 0);
+    static constexpr uint32_t S_BYTES = S_BAR + 512;
+    static constexpr int THREADS = 32 * (E4M3 ? 14 : 10);
+};
+static_assert(Layout<false>::S_BYTES <= 232448 && Layout<true>::S_BYTES <= 232448, "shared memory");
+
+struct Desc {  // what a CTA leaves for the combine kernel
+    int32_t tail;         // its last item is cut after it: slot 2c + 1 holds the item's first part
+    int32_t head;         // slot 2c holds a part of an item begun before: 1, or 2 for its last part
+    int32_t row0, n_tok;  // of the item in slot 2c + 1
+    int32_t g;
+    int32_t status;
+    int32_t pad[2];
 };
 
-template <bool E4M3>
-__device__ __forceinline__ void cached8(const void *pages, const float *scales, int row, int lane,
-                                        float (&x)[8]) {
-    if constexpr (E4M3) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
-            static_cast<const unsigned char *>(pages) + (size_t)row * D + 8 * lane));
-        const float scale = __ldg(scales + row);
-        const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
-                (__nv_fp8x2_storage_t)(ww[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-            const float2 f = __half22float2(__half2(h2));
-            x[2 * i] = f.x * scale;
-            x[2 * i + 1] = f.y * scale;
+struct AttnParams {
+    CUtensorMap tm_q, tm_k, tm_v;
+    gdr_attn_paged_args a;
+    int shift;        // log2(page_size)
+    int n_rep, tile_tok;
+    int k_rows, v_rows;  // rows of a K and V box
+    int n_rows;       // rows of the cache: a row past the end reads as zeros
+    float scale_log2;
+    int *status;      // workspace
+    Desc *desc;       // [CTAs]
+    float *part_ml;   // [2 CTAs][128][2]: maximum (log2) and sum
+    float *part_o;    // [2 CTAs][128][256]
+};
+
+// sum_{i < n} floor((a i + b) / m), in the steps of Euclid's algorithm.
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (n > 0) {
+        if (a >= m) {
+            sum += n * (n - 1) / 2 * (a / m);
+            a %= m;
         }
-    } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(
-            static_cast<const __nv_bfloat16 *>(pages) + (size_t)row * D + 8 * lane));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        if (b >= m) {
+            sum += n * (b / m);
+            b %= m;
         }
+        const int64_t y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+// A sequence's lengths as the kernels use them.
+struct Seq {
+    int cu0, q, len;  // first packed row, new tokens, tokens before; len -1: lengths not usable
+    __device__ __forceinline__ void load(const AttnParams &p, int s) {
+        const gdr_kv_pages &c = p.a.pages;
+        cu0 = __ldg(c.cu_seqlens + s);
+        const int end = min(__ldg(c.cu_seqlens + s + 1), (int)p.a.n_tok);
+        cu0 = max(cu0, 0);
+        q = max(end - cu0, 0);
+        len = __ldg(p.a.cache_len + s);
+        const int64_t total = (int64_t)len + q;
+        if (len < 0 || total > ((int64_t)c.table_width << p.shift) || total > 0x7fffff00LL) len = -1;
+    }
+    __device__ __forceinline__ int tiles(const AttnParams &p) const {
+        return (q + p.tile_tok - 1) / p.tile_tok;
+    }
+    // Key tiles of query tile i.
+    __device__ __forceinline__ int keys(const AttnParams &p, int i) const {
+        if (len < 0) return 0;
+        const int64_t end = (int64_t)len + min((int64_t)q, (int64_t)(i + 1) * p.tile_tok);
+        return (int)((end + KEYS - 1) / KEYS);
+    }
+    // Cost of the first m query tiles of one kv head.
+    __device__ __forceinline__ int64_t cost(const AttnParams &p, int m) const {
+        int64_t u = (int64_t)m * ITEM_COST;
+        if (len < 0 || m == 0) return u;
+        const int whole = min(m, q / p.tile_tok);
+        u += floor_sum(whole, KEYS, p.tile_tok, (int64_t)len + p.tile_tok + KEYS - 1);
+        if (m > whole) u += ((int64_t)len + q + KEYS - 1) / KEYS;
+        return u;
+    }
+};
+
+// Where a CTA's stretch [lo, hi) begins: item (s, g, i), whose cost starts at u.
+struct Plan {
+    int64_t lo, hi, u;
+    int s, g, i;
+};
+
+struct Item {
+    int s, g;
+    int row0, n_tok;  // packed rows
+    int pos0;         // position of the first row's token
+    int end;          // keys attended by the last row
+    int n_kv;         // tiles of the whole item; 0: lengths not usable
+    int a, b;         // this CTA's tiles
+};
+
+// The items of a CTA's stretch, in order.  Every role walks them by itself.
+struct Walk {
+    Plan w;
+    Seq q;
+    int n_tiles;
+    __device__ __forceinline__ Walk(const AttnParams &p, const Plan *plan) : w(*plan), n_tiles(0) {
+        if (w.u < w.hi) {
+            q.load(p, w.s);
+            n_tiles = q.tiles(p);
+        }
+    }
+    __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
+        const gdr_kv_pages &c = p.a.pages;
+        while (w.u < w.hi) {
+            while (w.i >= n_tiles) {
+                w.i = 0;
+                if (n_tiles == 0 || ++w.g == c.H_kv) {
+                    w.g = 0;
+                    if (++w.s >= c.n_seq) return false;
+                    q.load(p, w.s);
+                    n_tiles = q.tiles(p);
+                }
+            }
+            const int first = w.i * p.tile_tok;
+            it.s = w.s;
+            it.g = w.g;
+            it.row0 = q.cu0 + first;
+            it.n_tok = min(p.tile_tok, q.q - first);
+            it.pos0 = q.len + first;
+            it.end = it.pos0 + it.n_tok;
+            it.n_kv = q.keys(p, w.i);
+            const int64_t from = max(w.lo - w.u - ITEM_COST, (int64_t)0);
+            const int64_t to = min(max(w.hi - w.u - ITEM_COST, (int64_t)0), (int64_t)it.n_kv);
+            const bool begins = w.u >= w.lo;
+            it.a = (int)min(from, (int64_t)it.n_kv);
+            it.b = (int)to;
+            w.u += ITEM_COST + it.n_kv;
+            ++w.i;
+            if (it.a < it.b || (it.n_kv == 0 && begins)) return true;
+        }
+        return false;
+    }
+};
+
+// One block-wide call: this CTA's stretch of the batch's cost.
+__device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Plan *plan) {
+    const gdr_kv_pages &c = p.a.pages;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = n_thr >> 5;
+    const int per = (c.n_seq + n_thr - 1) / n_thr;
+    const int s0 = (int)min((int64_t)tid * per, (int64_t)c.n_seq);
+    const int s1 = (int)min((int64_t)s0 + per, (int64_t)c.n_seq);
+    int64_t mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        Seq q;
+        q.load(p, s);
+        mine += c.H_kv * q.cost(p, q.tiles(p));
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kFullMask, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    if (tid == 0) *plan = Plan{0, 0, 0, 0, 0, 0};
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int i = 0; i < n_warps; ++i) {
+        if (i < warp) before += warp_sum[i];
+        total += warp_sum[i];
+    }
+    upto += before;
+    // (blockIdx * total could overflow.)
+    const int64_t n = gridDim.x, each = total / n, more = total - each * n;
+    const int64_t lo = blockIdx.x * each + min((int64_t)blockIdx.x, more);
+    const int64_t hi = lo + each + (blockIdx.x < more ? 1 : 0);
+    int64_t u = upto - mine;
+    if (lo < hi && u <= lo && lo < upto) {
+        for (int s = s0; s < s1; ++s) {
+            Seq q;
+            q.load(p, s);
+            const int n_tiles = q.tiles(p);
+            const int64_t head = q.cost(p, n_tiles), all = head * c.H_kv;
+            if (lo < u + all) {
+                const int g = (int)((lo - u) / head);
+                u += g * head;
+                int a = 0, b = n_tiles;  // the last tile that begins at or before lo
+                while (b - a > 1) {
+                    const int m = a + (b - a) / 2;
+                    if (u + q.cost(p, m) <= lo) a = m;
+                    else b = m;
+                }
+                *plan = Plan{lo, hi, u + q.cost(p, a), s, g, a};
+                break;
+            }
+            u += all;
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two f16 values as e4m3 codes in two parts, the second what the first leaves.
+__device__ __forceinline__ void split2(uint32_t h2, uint16_t &hi, uint16_t &lo) {
+    uint32_t back, rest;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h2));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h2), "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+// Uses of the ring by an item of n tiles, 4 a tile, in the order the MMA thread takes
+// them: K0, K1, V0, K2, V1, ..., V(n-1).
+__device__ __forceinline__ int use_k(int i) { return i == 0 ? 0 : 4 * i - 2; }
+__device__ __forceinline__ int use_v(int i, int n) { return i < n - 1 ? 4 * i + 4 : 4 * n - 2; }
+
+template <bool E4M3, bool OUT_BF16>
+__global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
+    attn_paged_kernel(const __grid_constant__ AttnParams p) {
+    using L = Layout<E4M3>;
+    constexpr int NSLOT = L::NSLOT;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::S_BAR);  // [NSLOT] slot landed
+    uint64_t *empty = full + NSLOT;    // [NSLOT] slot consumed
+    uint64_t *q_full = empty + NSLOT;  // Q tile landed
+    uint64_t *q_split = q_full + 1;    // Q tile split in hi and lo (4 warps)
+    uint64_t *q_free = q_full + 2;     // the item's S products are done
+    uint64_t *bar_s = q_full + 3;      // [2] S of a tile in TMEM
+    uint64_t *bar_p = q_full + 5;      // [2] P of a tile in TMEM, O rescaled (8 warps)
+    uint64_t *bar_o = q_full + 7;      // [2] O += P V of a tile done
+    uint64_t *o_free = q_full + 9;     // the item's O has been read (8 warps)
+    uint64_t *sc_full = q_full + 10;   // [2] scales of a tile prepared (4 warps)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::S_BAR + 256);
+    Plan *plan = reinterpret_cast<Plan *>(sm + L::S_BAR + 272);
+    int64_t *warp_sum = reinterpret_cast<int64_t *>(sm + L::S_BAR + 320);  // [14]
+    float *red = reinterpret_cast<float *>(sm + L::S_RED);
+    const gdr_kv_pages &c = p.a.pages;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t sbase = smem_u32(sm);
+    const uint32_t ring = sbase + L::S_RING, sq = sbase + L::S_Q;
+
+    if (warp == 0) tmem_alloc(tmem_slot, TM_COLS);
+    if (tid == 0) {
+        for (int i = 0; i < NSLOT; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_split, 4);
+        mbar_init(q_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_s + i, 1);
+            mbar_init(bar_p + i, SOFTMAX_WARPS);
+            mbar_init(bar_o + i, 1);
+            mbar_init(sc_full + i, 4);
+        }
+        mbar_init(o_free, SOFTMAX_WARPS);
+        mbar_fence_init();
+    }
+    wait_for_predecessor();
+    release_dependents();
+    Desc *desc = p.desc + blockIdx.x;
+    if (tid == 0) *desc = Desc{};
+    make_plan(p, L::THREADS, warp_sum, plan);
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = *tmem_slot;
+    auto report = [&](int status) { atomicMax(&desc->status, status); };
+    auto full_wait = [&](int use) {
+        return mbar_wait(full + use % NSLOT, (uint32_t)(use / NSLOT) & 1u, kWaitNs);
+    };
+    // The swizzled tiles must start on 1024-byte boundaries.
+    const bool usable = (sbase & 1023u) == 0;
+    if (!usable && tid == 0) report(GDR_ERR_CUDA);
+
+    Walk walk(p, plan);
+    Item it;
+    if (!usable) {
+        // nothing runs
+    } else if (warp == W_LOAD) {
+        // ---------------------------------------------------------- loads
+        // Lane 0 keeps the barriers; every lane issues its boxes of a slot.
+        bool ok = true, bad = false;
+        int n_use = 0, n_item = 0;
+        if (lane == 0) {
+            tma_prefetch_map(&p.tm_q);
+            tma_prefetch_map(&p.tm_k);
+            tma_prefetch_map(&p.tm_v);
+            fence_proxy_async_global();
+        }
+        __syncwarp();
+        const int kr = p.k_rows, vr = p.v_rows;
+        while (ok && walk.next(p, it)) {
+            if (it.n_kv == 0) {
+                bad = true;
+                continue;
+            }
+            // Cache row of each 16 keys of a tile, in lanes 0 .. 7; past the cache's end
+            // (zeros) for a page that does not exist.
+            auto page_row = [&](int j) {
+                const int key = j * KEYS + 16 * lane;
+                int row = p.n_rows;
+                if (lane < 8 && j < it.b && key < it.end) {
+                    const int r = cache_row(c, p.shift, it.s, it.g, key);
+                    if (r >= 0) row = r;
+                    else bad = true;
+                }
+                return row;
+            };
+            // One slot: n_box rows of boxes with n_col boxes each.
+            auto acquire = [&](int use) {
+                if (use >= NSLOT && lane == 0)
+                    ok = mbar_wait(empty + use % NSLOT, (uint32_t)(use / NSLOT - 1) & 1u, kWaitNs);
+                ok = __shfl_sync(kFullMask, ok, 0);
+                return ok;
+            };
+            auto load_k = [&](int j, int use0, int row) {
+                const int n = min(KEYS, it.end - j * KEYS);
+                const int parts = (n + kr - 1) / kr;
+                constexpr int NCOL = E4M3 ? 1 : 2;
+                for (int h = 0; h < 2; ++h) {
+                    const int use = use0 + h;
+                    if (!acquire(use)) return;
+                    uint64_t *bar = full + use % NSLOT;
+                    if (lane == 0) bulk_expect(bar, (uint32_t)(parts * NCOL * kr * 128));
+                    __syncwarp();
+                    const int part = lane / NCOL, col = lane % NCOL;
+                    const int r = __shfl_sync(kFullMask, row, (part * (kr >> 4)) & 7);
+                    if (part < parts)
+                        tma_load_2d(ring + (use % NSLOT) * L::SLOT + col * BOX + part * kr * 128,
+                                    &p.tm_k, h * 128 + col * 64, r, bar);
+                    n_use = use + 1;
+                }
+            };
+            auto load_v = [&](int j, int use0, int row) {
+                const int n = min(KEYS, it.end - j * KEYS);
+                for (int h = 0; h < 2; ++h) {
+                    const int use = use0 + h;
+                    if (!acquire(use)) return;
+                    uint64_t *bar = full + use % NSLOT;
+                    const uint32_t dst = ring + (use % NSLOT) * L::SLOT;
+                    constexpr int NCOL = E4M3 ? 1 : 4;
+                    const int keys = E4M3 ? n : max(0, min(64, n - 64 * h));
+                    const int parts = (keys + vr - 1) / vr;
+                    if (lane == 0) {
+                        if (parts > 0) bulk_expect(bar, (uint32_t)(parts * NCOL * vr * 128));
+                        else mbar_arrive(bar);
+                    }
+                    __syncwarp();
+                    const int part = lane / NCOL, col = lane % NCOL;
+                    const int r = __shfl_sync(kFullMask, row, (part * (vr >> 4) + (E4M3 ? 0 : 4 * h)) & 7);
+                    if (part < parts)
+                        tma_load_2d(dst + col * (BOX / 2) + part * vr * 128, &p.tm_v,
+                                    E4M3 ? h * 128 : col * 64, r, bar);
+                    n_use = use + 1;
+                }
+            };
+            const int n = it.b - it.a, base = n_use;
+            int row = page_row(it.a), row1 = page_row(it.a + 1);
+            if (n_item > 0) {
+                if (lane == 0) ok = mbar_wait(q_free, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                ok = __shfl_sync(kFullMask, ok, 0);
+                if (!ok) break;
+            }
+            ++n_item;
+            if (lane == 0) {
+                bulk_expect(q_full, (uint32_t)(4 * 128 * p.n_rep * p.tile_tok));
+                for (int b = 0; b < 4; ++b)
+                    tma_load_3d(sq + b * BOX, &p.tm_q, b * 64, it.g * p.n_rep, it.row0, q_full);
+            }
+            __syncwarp();
+            load_k(it.a, base + use_k(0), row);
+            for (int i = 0; i < n && ok; ++i) {
+                const int row2 = page_row(it.a + i + 2);
+                if (i + 1 < n) load_k(it.a + i + 1, base + use_k(i + 1), row1);
+                if (ok) load_v(it.a + i, base + use_v(i, n), row);
+                row = row1;
+                row1 = row2;
+            }
+        }
+        bad = __any_sync(kFullMask, bad);
+        if (lane == 0) {
+            if (bad) report(kBadPage);
+            if (!ok) {
+                report(kTimeout);
+                // No copy may land after the CTA ends.
+                if (n_item > 0) mbar_wait(q_full, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                for (int u = max(0, n_use - NSLOT); u < n_use; ++u) full_wait(u);
+            }
+            // Nor may an arrival that a commit owes: the last use of every slot, the
+            // last item's Q.
+            const uint64_t lim = ok ? kWaitNs : kDrainNs;
+            for (int u = max(0, n_use - NSLOT); u < n_use; ++u)
+                mbar_wait(empty + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, lim);
+            if (n_item > 0) mbar_wait(q_free, (uint32_t)(n_item - 1) & 1u, lim);
+        }
+        __syncwarp();
+    } else if (warp == W_MMA) {
+        // ------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr Kind KIND = E4M3 ? Kind::E4M3 : Kind::BF16;
+            constexpr uint32_t ID_S = instr_desc<KIND>(128, KEYS, false, false);
+            constexpr uint32_t ID_O = instr_desc<KIND>(128, E4M3 ? 128 : 256, false, true);
+            bool ok = true;
+            int jt = 0, base = 0, n_item = 0;
+            while (ok && walk.next(p, it)) {
+                if (it.n_kv == 0) continue;
+                const int n = it.b - it.a;
+                ok = mbar_wait(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u, kWaitNs);
+                auto score = [&](int i) {  // S of the item's tile i
+                    const uint32_t d = tm + TM_S + 128 * ((jt + i) & 1);
+                    const int u0 = base + use_k(i);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (!full_wait(u0 + h)) return false;
+                        fence_after_sync();
+                        const uint32_t kb = ring + ((u0 + h) % NSLOT) * L::SLOT;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            // bf16: box k / 4 of the half; e4m3: the hi, then the lo part
+                            const uint32_t qa = sq + (2 * h + (k >> 2)) * BOX + (k & 3) * 32;
+                            const uint32_t ka = kb + (E4M3 ? 0 : (k >> 2) * BOX) + (k & 3) * 32;
+                            mma<KIND>(d, smem_desc_sw128(qa, 16, 1024), smem_desc_sw128(ka, 16, 1024),
+                                      ID_S, (h | k) ? 1u : 0u);
+                        }
+                    }
+                    commit(smem_u32(bar_s + ((jt + i) & 1)));
+                    commit(smem_u32(empty + u0 % NSLOT));
+                    commit(smem_u32(empty + (u0 + 1) % NSLOT));
+                    if (i == n - 1) commit(smem_u32(q_free));
+                    return true;
+                };
+                ok = ok && score(0);
+                for (int i = 0; i < n && ok; ++i) {
+                    if (i + 1 < n) ok = score(i + 1);
+                    if (ok && i == 0 && n_item > 0) ok = mbar_wait(o_free, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                    const int j = jt + i, u0 = base + use_v(i, n);
+                    ok = ok && mbar_wait(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
+                    const int keys = min(KEYS, it.end - (it.a + i) * KEYS);
+                    const uint32_t pt = tm + TM_S + 128 * (j & 1);
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = full_wait(u0 + h);
+                        if (!ok) break;
+                        fence_after_sync();
+                        const uint32_t vb = ring + ((u0 + h) % NSLOT) * L::SLOT;
+                        if constexpr (!E4M3) {
+                            const int steps = min(4, (keys - 64 * h + 15) >> 4);
+                            for (int k = 0; k < steps; ++k)
+                                mma_ta(tm + TM_O, pt + 64 * h + 8 * k,
+                                       smem_desc_sw128(vb + k * 2048, BOX / 2, 1024), ID_O,
+                                       (i | h | k) ? 1u : 0u);
+                        } else {
+                            const int steps = (keys + 31) >> 5;
+                            for (int part = 0; part < 2; ++part)
+                                for (int k = 0; k < steps; ++k)
+                                    mma_ta_e4m3(tm + TM_O + 128 * h,
+                                                pt + 64 * (k >> 1) + 16 * part + 8 * (k & 1),
+                                                smem_desc_sw128(vb + k * 4096, BOX, 1024), ID_O,
+                                                (i | part | k) ? 1u : 0u);
+                        }
+                    }
+                    if (!ok) break;
+                    commit(smem_u32(bar_o + (j & 1)));
+                    commit(smem_u32(empty + u0 % NSLOT));
+                    commit(smem_u32(empty + (u0 + 1) % NSLOT));
+                }
+                jt += n;
+                base += 4 * n;
+                ++n_item;
+            }
+            if (!ok) report(kTimeout);
+        }
+        __syncwarp();
+    } else if (E4M3 && warp >= W_AUX) {
+        // -------------------------------------- Q in two parts, and the scales
+        const int t = tid - 32 * W_AUX;  // row of Q, key of a tile
+        float *scales = reinterpret_cast<float *>(sm + L::S_SCALE);
+        float *rowk = reinterpret_cast<float *>(sm + L::S_ROWK);
+        bool ok = true;
+        int jt = 0, n_item = 0;
+        while (ok && walk.next(p, it)) {
+            if (it.n_kv == 0) continue;
+            ok = __all_sync(kFullMask, mbar_wait(q_full, (uint32_t)n_item & 1u, kWaitNs));
+            if (!ok) break;
+            // Row t: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (t % 8).
+            const uint32_t row = sq + t * 128;
+            auto chunk = [&](int b, int j) { return row + b * BOX + ((j ^ (t & 7)) << 4); };
+            uint32_t top = 0;  // largest magnitude, as bf16 bits
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 v = ld_shared16(chunk(b, j));
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                }
+            // A power of two that takes the largest value into [128, 256).
+            const int e = min(max((int)max(top >> 16, top & 0xffffu) >> 7, 8), 254);
+            const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+            rowk[(n_item & 1) * ROWS + t] = __uint_as_float((uint32_t)(e - 7) << 23);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = ld_shared16(chunk(2 * h + (j >> 3), j & 7));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // 16 values
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint4 v = x[2 * j + (w >> 1)];
+                        const uint32_t v0 = w & 1 ? v.z : v.x, v1 = w & 1 ? v.w : v.y;
+                        uint16_t h0, h1, l0, l1;
+                        split2(f16x2(__uint_as_float(v0 << 16) * up,
+                                     __uint_as_float(v0 & 0xffff0000u) * up), h0, l0);
+                        split2(f16x2(__uint_as_float(v1 << 16) * up,
+                                     __uint_as_float(v1 & 0xffff0000u) * up), h1, l1);
+                        hi[w] = h0 | (uint32_t)h1 << 16;
+                        lo[w] = l0 | (uint32_t)l1 << 16;
+                    }
+                    st_shared16(chunk(2 * h, j), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    st_shared16(chunk(2 * h + 1, j), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                }
+            }
+            fence_smem_to_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_split);
+            // Scales of key t of each tile, fetched a tile ahead.
+            auto fetch = [&](int j, float &ks, float &vs) {
+                const int key = j * KEYS + t;
+                ks = vs = 0.f;
+                if (j < it.b && key < it.end) {
+                    const int r = cache_row(c, p.shift, it.s, it.g, key);
+                    if (r >= 0) {
+                        ks = __ldg(c.k_scale + r);
+                        vs = __ldg(c.v_scale + r);
+                    }
+                }
+            };
+            float ks, vs;
+            fetch(it.a, ks, vs);
+            for (int j = it.a; j < it.b; ++j, ++jt) {
+                float ks1, vs1;
+                fetch(j + 1, ks1, vs1);
+                // The stage was read by the softmax two tiles back.
+                if (jt >= 2)
+                    ok = __all_sync(kFullMask,
+                                    mbar_wait(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs));
+                if (!ok) break;
+                float *st = scales + (jt & 1) * 3 * KEYS;
+                // The smallest scale that an append writes stands for zero too: it keeps
+                // the key in the softmax's sum.
+                vs = fmaxf(vs, kScaleMin);
+                st[t] = ks * p.scale_log2;
+                st[KEYS + t] = log2f(vs);
+                st[2 * KEYS + t] = 1.f / vs;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full + (jt & 1));
+                ks = ks1;
+                vs = vs1;
+            }
+            ++n_item;
+        }
+        if (!ok && lane == 0) report(kTimeout);
+    } else if (warp < SOFTMAX_WARPS) {
+        // -------------------------------------------------------- softmax
+        // Warps w and w + 4 share rows 32 (w % 4) ..; each takes 64 of a tile's keys and
+        // 128 of O's columns.  They agree on a row's maximum through red[], and to
+        // stop, at the same barrier.
+        //
+        // The reference maximum only moves when a tile's maximum passes it by
+        // more than kLazy (log2): then O and the sum are rescaled, which needs
+        // the tile before's product finished.  bf16 holds a weight of any size
+        // alike; the e4m3 parts hold 2^-9 .. 448, so there the weights sit 2^6 up
+        // and may grow by 2^2.
+        constexpr float kLazy = E4M3 ? 2.f : 8.f;
+        constexpr float kUp = E4M3 ? 6.f : 0.f;
+        const int half = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
+        const int tok = r / p.n_rep, h = r - tok * p.n_rep;
+        const float *scales = reinterpret_cast<const float *>(sm + L::S_SCALE);
+        const float *rowk = reinterpret_cast<const float *>(sm + L::S_ROWK);
+        bool dead = false, fault = false;
+        int jt = 0, base = 0, n_item = 0;
+        auto wait_o = [&](int tile, uint64_t lim) {
+            return mbar_wait(bar_o + (tile & 1), (uint32_t)(tile >> 1) & 1u, lim);
+        };
+        while (!dead && walk.next(p, it)) {
+            const bool mine = tok < it.n_tok;  // this row exists
+            const bool some = __any_sync(kFullMask, mine);
+            const int64_t grow = it.row0 + tok;
+            const int gh = it.g * p.n_rep + h;
+            if (it.n_kv == 0) {
+                // Lengths that cannot be used: zeros.
+                if (mine) {
+                    for (int d = 128 * half; d < 128 * half + 128; d += 4) {
+                        using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
+                        Elem<T>::store4(static_cast<T *>(p.a.out) + grow * p.a.out_stride + gh * D + d,
+                                        make_float4(0.f, 0.f, 0.f, 0.f));
+                    }
+                    if (half == 0 && p.a.lse) p.a.lse[grow * p.a.lse_stride + gh] = -INFINITY;
+                }
+                continue;
+            }
+            const int n = it.b - it.a;
+            float m_ref = -INFINITY, l = 0.f;
+            float row_factor = 1.f;
+            for (int i = 0; i < n; ++i) {
+                const int j = jt + i, k0 = (it.a + i) * KEYS;
+                bool ok = mbar_wait(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
+                if (E4M3) ok = ok && mbar_wait(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
+                ok = __all_sync(kFullMask, ok);
+                float s[64];
+                float top = -INFINITY;
+                if (some && ok) {
+                    fence_after_sync();
+                    tmem_ld64(tm + lane_off + TM_S + 128 * (j & 1) + 64 * half, s);
+                    if constexpr (E4M3) {
+                        if (i == 0) row_factor = rowk[(n_item & 1) * ROWS + r];
+                        const float4 *sk = reinterpret_cast<const float4 *>(scales + (j & 1) * 3 * KEYS + 64 * half);
+                        const float4 *lv = sk + KEYS / 4;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float4 a = sk[x], b = lv[x];
+                            s[4 * x] = fmaf(s[4 * x] * row_factor, a.x, b.x);
+                            s[4 * x + 1] = fmaf(s[4 * x + 1] * row_factor, a.y, b.y);
+                            s[4 * x + 2] = fmaf(s[4 * x + 2] * row_factor, a.z, b.z);
+                            s[4 * x + 3] = fmaf(s[4 * x + 3] * row_factor, a.w, b.w);
+                        }
+                    }
+                    // Keys this row attends, of this thread's 64.
+                    const int lim = (mine ? it.pos0 + tok + 1 - k0 : 0) - 64 * half;
+                    if (__any_sync(kFullMask, lim < 64)) {
+#pragma unroll
+                        for (int x = 0; x < 64; ++x)
+                            if (x >= lim) s[x] = -INFINITY;
+                    }
+                    float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int x = 4; x < 64; x += 4) {
+                        t4[0] = fmaxf(t4[0], s[x]);
+                        t4[1] = fmaxf(t4[1], s[x + 1]);
+                        t4[2] = fmaxf(t4[2], s[x + 2]);
+                        t4[3] = fmaxf(t4[3], s[x + 3]);
+                    }
+                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    if (!E4M3) top *= p.scale_log2;
+                    red[((j & 1) * 2 + half) * ROWS + r] = top;
+                }
+                dead = group_sync_or(1 + quad, 64, !ok || fault);
+                if (dead) break;
+                if (some) {
+                    top = fmaxf(top, red[((j & 1) * 2 + (half ^ 1)) * ROWS + r]);
+                    const bool first = m_ref == -INFINITY;
+                    const bool moves = !first && top > m_ref + kLazy;
+                    const float alpha = moves ? exp2_fast(m_ref - top) : 1.f;
+                    if (first || moves) m_ref = top;
+                    l *= alpha;
+                    const bool rescale = __any_sync(kFullMask, moves) && i > 0;
+                    // -inf (nothing attended yet) as 0: every exponent below is -inf then.
+                    const float sub = (m_ref == -INFINITY ? 0.f : m_ref) - kUp;
+                    uint32_t pk[32];
+                    float l2[2] = {0.f, 0.f};
+                    if constexpr (!E4M3) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const float a = exp2_fast(fmaf(s[2 * x], p.scale_log2, -sub));
+                            const float b = exp2_fast(fmaf(s[2 * x + 1], p.scale_log2, -sub));
+                            l2[0] += a;
+                            l2[1] += b;
+                            pk[x] = bf16x2(a, b);
+                        }
+                    } else {
+                        const float4 *rs = reinterpret_cast<const float4 *>(scales + ((j & 1) * 3 + 2) * KEYS + 64 * half);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float4 f = rs[x];
+                            const float a = exp2_fast(s[4 * x] - sub), b = exp2_fast(s[4 * x + 1] - sub);
+                            const float d = exp2_fast(s[4 * x + 2] - sub), e = exp2_fast(s[4 * x + 3] - sub);
+                            l2[0] = fmaf(a, f.x, l2[0]);
+                            l2[1] = fmaf(b, f.y, l2[1]);
+                            l2[0] = fmaf(d, f.z, l2[0]);
+                            l2[1] = fmaf(e, f.w, l2[1]);
+                            uint16_t h0, h1, l0, l1;
+                            split2(f16x2(a, b), h0, l0);
+                            split2(f16x2(d, e), h1, l1);
+                            pk[x] = h0 | (uint32_t)h1 << 16;
+                            pk[16 + x] = l0 | (uint32_t)l1 << 16;
+                        }
+                    }
+                    l += l2[0] + l2[1];
+                    // Over S: both warps of the rows have read it (the barrier above).
+                    {
+                        float pf[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) pf[x] = __uint_as_float(pk[x]);
+                        __syncwarp();
+                        tmem_st32(tm + lane_off + TM_S + 128 * (j & 1) + 64 * half, pf);
+                    }
+                    if (rescale) {
+                        fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs));
+                        if (!fault) {
+                            fence_after_sync();
+#pragma unroll 1
+                            for (int x = 0; x < 128; x += 32) {
+                                float o[32];
+                                tmem_ld32(tm + lane_off + TM_O + 128 * half + x, o);
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) o[y] *= alpha;
+                                tmem_st32(tm + lane_off + TM_O + 128 * half + x, o);
+                            }
+                        }
+                    }
+                }
+                // The MMA takes V's keys in steps of 16 (32 codes): what pages hold between
+                // the sequence's end and the step's becomes zero.
+                const int keys = it.end - k0;
+                constexpr int STEP = E4M3 ? 32 : 16;
+                if (keys < KEYS && (keys & (STEP - 1))) {
+                    const int up = (keys + STEP - 1) & ~(STEP - 1);
+                    const int u0 = base + use_v(i, n);
+                    const int u = E4M3 ? u0 : u0 + (keys >> 6);
+                    bool okv = full_wait(u);
+                    if (E4M3) okv = okv && full_wait(u0 + 1);
+                    fault = fault || !__all_sync(kFullMask, okv);
+                    if (!fault) {
+                        // 32 16-byte chunks a key: bf16, 4 boxes of 8; codes, 2 slots of 8.
+                        constexpr int CH = E4M3 ? 16 : 32;
+                        for (int x = tid; x < (up - keys) * CH; x += 32 * SOFTMAX_WARPS) {
+                            const int key = keys + x / CH, ch = x % CH;
+                            const int uu = E4M3 ? u0 + (ch >> 3) : u;
+                            const uint32_t at = ring + (uu % NSLOT) * L::SLOT +
+                                                (E4M3 ? 0 : (ch >> 3) * (BOX / 2)) +
+                                                (E4M3 ? key : key & 63) * 128 + (ch & 7) * 16;
+                            st_shared16(at, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    fence_smem_to_async();
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_p + (j & 1));
+            }
+            if (dead) break;
+            jt += n;
+            base += 4 * n;
+            ++n_item;
+            // The item's end: the row's sum over both threads, then O.
+            red[((jt & 1) * 2 + half) * ROWS + r] = l;
+            const bool ok = wait_o(jt - 1, kWaitNs);
+            dead = group_sync_or(1 + quad, 64, !ok || fault);
+            if (dead) break;
+            l += red[((jt & 1) * 2 + (half ^ 1)) * ROWS + r];
+            group_sync_or(1 + quad, 64, false);  // the next tile writes there
+            fence_after_sync();
+            const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
+            const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (some) {
+#pragma unroll 1
+                for (int x = 0; x < 128; x += 32) {
+                    float o[32];
+                    __syncwarp();
+                    tmem_ld32(tm + lane_off + TM_O + 128 * half + x, o);
+                    const int d0 = 128 * half + x;
+                    if (!mine) continue;
+                    if (!whole) {
+                        float *po = p.part_o + ((size_t)slot * ROWS + r) * D + d0;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4)
+                            *reinterpret_cast<float4 *>(po + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                        continue;
+                    }
+                    const __nv_bfloat16 *gate =
+                        p.a.gate ? static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + d0
+                                 : nullptr;
+                    const int64_t at = grow * p.a.out_stride + gh * D + d0;
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) v[z] = o[y + z] * inv;
+                        if (gate) {
+                            const uint4 g8 = __ldg(reinterpret_cast<const uint4 *>(gate + y));
+                            const uint32_t gw[4] = {g8.x, g8.y, g8.z, g8.w};
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) {
+                                const float gt = __uint_as_float(z & 1 ? gw[z >> 1] & 0xffff0000u : gw[z >> 1] << 16);
+                                v[z] = __fdividef(v[z], 1.f + __expf(-gt));
+                            }
+                        }
+                        if constexpr (OUT_BF16) {
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at + y) =
+                                make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                           bf16x2(v[6], v[7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at + y);
+                            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                    }
+                }
+                if (mine && half == 0) {
+                    if (!whole) {
+                        float *ml = p.part_ml + ((size_t)slot * ROWS + r) * 2;
+                        ml[0] = m_ref - kUp;
+                        ml[1] = l;
+                    } else if (p.a.lse) {
+                        p.a.lse[grow * p.a.lse_stride + gh] =
+                            l > 0.f ? (m_ref - kUp + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    }
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            if (!whole && tid == 0) {
+                if (!begins) {
+                    desc->head = ends ? 2 : 1;
+                } else {
+                    desc->tail = 1;
+                    desc->row0 = it.row0;
+                    desc->n_tok = it.n_tok;
+                    desc->g = it.g;
+                }
+            }
+        }
+        if ((dead || fault) && lane == 0) report(kTimeout);
+        // The product before the last is waited for by nobody: its commit must land too.
+        if (jt >= 2) wait_o(jt - 2, dead ? kDrainNs : kWaitNs);
+        if (dead && jt >= 1) wait_o(jt - 1, kDrainNs);
+    }
+
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) {
+        fence_after_sync();
+        tmem_free(tm, TM_COLS);
     }
 }
 
-template <bool E4M3, typename TOUT>
-__global__ void __launch_bounds__(256) attn_paged_kernel(const AttnParams p) {
+// --------------------------------------------------------------- combine
+
+// Block b joins a quarter of the rows of the item that CTA b / 4 began and did not end, a
+// row a warp: y = (sum_i 2^{m_i - m} O_i) / (sum_i 2^{m_i - m} l_i) * sigmoid(gate).
+constexpr int COMBINE_SPLIT = 4;
+constexpr int COMBINE_WARPS = 8;
+template <bool OUT_BF16>
+__global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const AttnParams p, int n_cta) {
     wait_for_predecessor();
-    const gdr_attn_paged_args &a = p.a;
-    const gdr_kv_pages &c = a.pages;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (w >= a.n_tok * a.H_q) return;
-    const int64_t t = w / a.H_q;
-    const int h = (int)(w - t * a.H_q), g = h / (a.H_q / c.H_kv);
-    const int s = find_sequence(c.cu_seqlens, c.n_seq, (int)t);
-    if (s >= c.n_seq) return;
-    const int i = (int)t - __ldg(c.cu_seqlens + s);
-    if (i < 0) return;
-    const int64_t last = (int64_t)__ldg(a.cache_len + s) + i;
-    float q[8], o[8] = {}, m = -INFINITY, l = 0.f;
-    cached8<false>(static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride + h * D, nullptr, 0,
-                   lane, q);
-    for (int64_t j = 0; j <= last; ++j) {
-        const int row = cache_row(c, p.shift, s, g, j);
-        if (row < 0) {
-            if (lane == 0) *p.status = kBadPage;
+    release_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cta = blockIdx.x / COMBINE_SPLIT, share = blockIdx.x % COMBINE_SPLIT;
+    if (blockIdx.x == 0 && warp == 0) {
+        int st = 0;
+        for (int i = lane; i < n_cta; i += 32) st = max(st, p.desc[i].status);
+        st = __reduce_max_sync(kFullMask, st);
+        if (lane == 0) *p.status = st;
+    }
+    const Desc d = p.desc[cta];
+    if (!d.tail) return;
+    const int rows = d.n_tok * p.n_rep;
+    // The parts: slot 2 cta + 1, then slot 2 i of the CTAs after it up to the last part.
+    int last = cta;
+    for (int i0 = cta + 1; i0 < n_cta; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t ends = __ballot_sync(kFullMask, i < n_cta && p.desc[i].head == 2);
+        if (ends) {
+            last = i0 + __ffs(ends) - 1;
             break;
         }
-        float k[8], v[8];
-        cached8<E4M3>(c.k, c.k_scale, row, lane, k);
-        cached8<E4M3>(c.v, c.v_scale, row, lane, v);
-        float x = 0.f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) x = fmaf(q[d], k[d], x);
-        x = group_sum<32>(x) * a.scale;
-        const float top = fmaxf(m, x), f = expf(m - top), e = expf(x - top);
-        m = top;
-        l = fmaf(l, f, e);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[d] = fmaf(o[d], f, e * v[d]);
+        last = min(i0 + 31, n_cta - 1);
     }
-    if (last < 0 && lane == 0) *p.status = kBadPage;
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    const int64_t at = t * a.out_stride + h * D + 8 * lane;
+    for (int r = share + COMBINE_SPLIT * warp; r < rows; r += COMBINE_SPLIT * COMBINE_WARPS) {
+        const int tok = r / p.n_rep, h = r - tok * p.n_rep;
+        // The maximum and the sum over the parts, a part a lane.
+        float m = -INFINITY;
+        for (int i0 = cta; i0 <= last; i0 += 32) {
+            const int i = i0 + lane;
+            const bool has = i == cta || (i <= last && p.desc[min(i, last)].head != 0);
+            if (has) m = fmaxf(m, p.part_ml[((size_t)(2 * i + (i == cta)) * ROWS + r) * 2]);
+        }
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-        float y = o[d] * r;
-        if (a.gate)
-            y /= 1.f + expf(-__bfloat162float(static_cast<const __nv_bfloat16 *>(
-                           a.gate)[t * a.gate_stride + h * D + 8 * lane + d]));
-        Elem<TOUT>::store1(static_cast<TOUT *>(a.out) + at + d, y);
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+        float l = 0.f, o[8] = {};
+        for (int i0 = cta; i0 <= last; i0 += 32) {
+            const int i = i0 + lane;
+            const bool has = i == cta || (i <= last && p.desc[min(i, last)].head != 0);
+            float f = 0.f;
+            if (has) {
+                const float2 ml = *reinterpret_cast<const float2 *>(
+                    p.part_ml + ((size_t)(2 * i + (i == cta)) * ROWS + r) * 2);
+                // A part in which the row attends nothing has m = -inf and adds nothing.
+                f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+                l = fmaf(f, ml.y, l);
+            }
+            const int n = min(32, last - i0 + 1);
+#pragma unroll 4
+            for (int x = 0; x < n; ++x) {
+                const float fx = __shfl_sync(kFullMask, f, x);
+                if (fx == 0.f) continue;
+                const int ix = i0 + x;
+                const float4 *po = reinterpret_cast<const float4 *>(
+                    p.part_o + ((size_t)(2 * ix + (ix == cta)) * ROWS + r) * D + 8 * lane);
+                const float4 a = po[0], b = po[1];
+                o[0] = fmaf(fx, a.x, o[0]);
+                o[1] = fmaf(fx, a.y, o[1]);
+                o[2] = fmaf(fx, a.z, o[2]);
+                o[3] = fmaf(fx, a.w, o[3]);
+                o[4] = fmaf(fx, b.x, o[4]);
+                o[5] = fmaf(fx, b.y, o[5]);
+                o[6] = fmaf(fx, b.z, o[6]);
+                o[7] = fmaf(fx, b.w, o[7]);
+            }
+        }
+        l = group_sum<32>(l);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int64_t grow = d.row0 + tok;
+        const int gh = d.g * p.n_rep + h;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[x] *= inv;
+        if (p.a.gate) {
+            const uint4 g8 = __ldg(reinterpret_cast<const uint4 *>(
+                static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + 8 * lane));
+            const uint32_t gw[4] = {g8.x, g8.y, g8.z, g8.w};
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float gt = __uint_as_float(x & 1 ? gw[x >> 1] & 0xffff0000u : gw[x >> 1] << 16);
+                o[x] = __fdividef(o[x], 1.f + __expf(-gt));
+            }
+        }
+        const int64_t at = grow * p.a.out_stride + gh * D + 8 * lane;
+        if constexpr (OUT_BF16) {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at) =
+                make_uint4(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]), bf16x2(o[4], o[5]), bf16x2(o[6], o[7]));
+        } else {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at);
+            dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+        if (lane == 0 && p.a.lse)
+            p.a.lse[grow * p.a.lse_stride + gh] =
+                l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
-    if (lane == 0 && a.lse) a.lse[t * a.lse_stride + h] = m + logf(l);
 }
 
+namespace {
+
+constexpr size_t WS_DESC = 256;
+size_t ws_ml(int n_cta) { return WS_DESC + (((size_t)n_cta * sizeof(Desc) + 255) & ~(size_t)255); }
+size_t ws_o(int n_cta) { return ws_ml(n_cta) + (size_t)2 * n_cta * ROWS * 2 * 4; }
+
+template <bool E4M3, bool OUT_BF16>
+cudaError_t launch_attn(const AttnParams &p, int n_cta, cudaStream_t s) {
+    using L = Layout<E4M3>;
+    const auto kern = attn_paged_kernel<E4M3, OUT_BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::S_BYTES);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return e;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n_cta);
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::S_BYTES;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e == cudaSuccess) {
+        cfg.gridDim = dim3((unsigned)(n_cta * COMBINE_SPLIT));
+        cfg.blockDim = dim3(32 * COMBINE_WARPS);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, attn_paged_combine<OUT_BF16>, p, n_cta);
+    }
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+}  // namespace
 }  // namespace paged
 
-size_t attn_paged_workspace_bytes(int n_sm) { return 256; }
+size_t attn_paged_workspace_bytes(int n_sm) {
+    return paged::ws_o(n_sm) + (size_t)2 * n_sm * paged::ROWS * paged::D * 4;
+}
 
 cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cudaStream_t s) {
-    paged::AttnParams p = {};
+    using namespace paged;
+    const gdr_kv_pages &c = a->pages;
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return cudaGetLastError();
+    AttnParams p = {};
     p.a = *a;
-    p.shift = paged::log2_of(a->pages.page_size);
-    p.status = static_cast<int *>(workspace);
-    cudaError_t e = cudaMemsetAsync(workspace, 0, 4, s);
-    if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((a->n_tok * a->H_q + 7) / 8);
-    const bool codes = a->pages.kv_dtype == GDR_E4M3, b = a->out_dtype == GDR_BF16;
-    if (codes && b) paged::attn_paged_kernel<true, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    if (codes && !b) paged::attn_paged_kernel<true, float><<<grid, 256, 0, s>>>(p);
-    if (!codes && b) paged::attn_paged_kernel<false, __nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    if (!codes && !b) paged::attn_paged_kernel<false, float><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    p.shift = log2_of(c.page_size);
+    p.n_rep = a->H_q / c.H_kv;
+    p.tile_tok = ROWS / p.n_rep;
+    const bool codes = c.kv_dtype == GDR_E4M3;
+    p.k_rows = c.page_size < KEYS ? c.page_size : KEYS;
+    const int v_keys = codes ? KEYS : KEYS / 2;  // keys of a V slot
+    p.v_rows = c.page_size < v_keys ? c.page_size : v_keys;
+    p.n_rows = c.n_pages * c.H_kv * c.page_size;
+    p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    p.status = reinterpret_cast<int *>(ws);
+    p.desc = reinterpret_cast<Desc *>(ws + WS_DESC);
+    p.part_ml = reinterpret_cast<float *>(ws + ws_ml(n_sm));
+    p.part_o = reinterpret_cast<float *>(ws + ws_o(n_sm));
+    const bool maps =
+        encode_bf16_3d(&p.tm_q, a->q, D, a->H_q, a->n_tok, (uint64_t)a->q_stride * 2, 64, p.n_rep, p.tile_tok) &&
+        (codes ? encode_u8_2d(&p.tm_k, c.k, D, p.n_rows, 128, p.k_rows) &&
+                     encode_u8_2d(&p.tm_v, c.v, D, p.n_rows, 128, p.v_rows)
+               : encode_bf16_2d(&p.tm_k, c.k, D, p.n_rows, D * 2, 64, p.k_rows) &&
+                     encode_bf16_2d(&p.tm_v, c.v, D, p.n_rows, D * 2, 64, p.v_rows));
+    if (!maps) return cudaErrorInvalidValue;
+    const bool bf16 = a->out_dtype == GDR_BF16;
+    if (codes) return bf16 ? launch_attn<true, true>(p, n_sm, s) : launch_attn<true, false>(p, n_sm, s);
+    return bf16 ? launch_attn<false, true>(p, n_sm, s) : launch_attn<false, false>(p, n_sm, s);
 }
 
 }  // namespace gdr

@@ -26,7 +26,6 @@ namespace paged {
 constexpr int TOKENS = 4;
 constexpr int WARPS = 8;
 constexpr float kE4m3Max = 448.f;
-constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40: rows of zeros keep a usable scale
 
 struct AppendParams {
     gdr_kv_append_args a;

@@ -10,6 +10,7 @@ namespace paged {
 
 constexpr int D = 256;
 constexpr int kBadPage = GDR_ERR_INVALID_ARG;
+constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40: a row of zeros keeps a usable scale
 
 // The sequence that owns packed row t: the s with cu[s] <= t < cu[s + 1], or n_seq
 // when no sequence owns it.  One whole warp calls it; every lane gets s.  cu

@@ -15,8 +15,8 @@ Bounds, element by element (u8 = 2^-8, half a step of bf16 relative to the value
       rounded to 8 significant bits, so
           |y - ref| <= (u8 + 2 d + 2^-19) sum_j P_j |v_j|   (times the gate)
       and u8 |y| more for a bf16 output.  Over a code cache the weight that is
-      rounded is P_j * v_scale_j, in two e4m3 parts whose smallest step is 2^-9 at a
-      scale where the row's reference weight is 2^6, and the reference is within 2^2 of the
+      rounded is P_j * v_scale_j, first to f16 (2^-11) and then in two e4m3 parts (2^-4 of
+      2^-4: u8 again); their smallest step is 2^-9 at a scale where the row's reference weight is 2^6, and the reference is within 2^2 of the
       largest weight: 2^-14 of the largest P_j v_scale_j per code, at most.
   A relative L2 over all rows: the roundings are independent and uniform, u8 / sqrt(3)
       each at most, for the weights and again for a bf16 output.
@@ -162,7 +162,8 @@ class Problem:
                 ref_lse = torch.logsumexp(sc, -1)
                 P = torch.exp(sc - ref_lse[..., None])
                 y = torch.einsum("igrt,tgd->igrd", P, v)
-                tol = (U8 + 2 * d + 2.0 ** -19) * torch.einsum("igrt,tgd->igrd", P, v.abs())
+                part = 2.0 ** -11 if self.kind == "e4m3" else 0.0
+                tol = (U8 + part + 2 * d + 2.0 ** -19) * torch.einsum("igrt,tgd->igrd", P, v.abs())
                 if self.kind == "e4m3":
                     top = (P * vs.t()[None, :, None]).amax(-1)
                     codes = (v / vs[..., None]).abs().sum(0)

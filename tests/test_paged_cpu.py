@@ -89,6 +89,8 @@ PAGES = [
     ("scales_with_bf16", dict(kv_dtype=1), INVALID),
     ("codes_without_scale", dict(v_scale=None), INVALID),
     ("null_pages", dict(k=None), INVALID),
+    ("no_pages", dict(n_pages=0), INVALID),
+    ("no_table", dict(table_width=0), INVALID),
     ("null_table", dict(page_table=None), INVALID),
     ("null_cu", dict(cu_seqlens=None), INVALID),
     ("table_stride_small", dict(table_stride=3), INVALID),
