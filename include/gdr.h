@@ -432,8 +432,9 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspac
  *
  *   k, v             [n_pages, H_kv, page_size, d] in kv_dtype, packed, 16-byte
  *                    aligned
- *   k_scale, v_scale [n_pages, H_kv, page_size] fp32, for GDR_E4M3 only (NULL
- *                    for GDR_BF16): row r stands for scale[r] * codes[r][0..d)
+ *   k_scale, v_scale [n_pages, H_kv, page_size] fp32, 16-byte aligned, for
+ *                    GDR_E4M3 only (NULL for GDR_BF16): row r stands for
+ *                    scale[r] * codes[r][0..d)
  *   page_table       device int32 [n_seq, table_width], row stride table_stride
  *                    (0 = table_width); entries past a sequence's last page are
  *                    not read

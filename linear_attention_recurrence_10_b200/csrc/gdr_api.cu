@@ -491,10 +491,9 @@ static gdr_status pages_pointers(const gdr_kv_pages *g) {
     if (!g->cu_seqlens || !g->k || !g->v || !g->page_table) return GDR_ERR_INVALID_ARG;
     if (g->kv_dtype == GDR_E4M3 ? (!g->k_scale || !g->v_scale) : (g->k_scale || g->v_scale))
         return GDR_ERR_INVALID_ARG;
-    if (!aligned16(g->k) || !aligned16(g->v)) return GDR_ERR_MISALIGNED;
-    if (!aligned4(g->k_scale) || !aligned4(g->v_scale) || !aligned4(g->page_table) ||
-        !aligned4(g->cu_seqlens))
+    if (!aligned16(g->k) || !aligned16(g->v) || !aligned16(g->k_scale) || !aligned16(g->v_scale))
         return GDR_ERR_MISALIGNED;
+    if (!aligned4(g->page_table) || !aligned4(g->cu_seqlens)) return GDR_ERR_MISALIGNED;
     return GDR_OK;
 }
 

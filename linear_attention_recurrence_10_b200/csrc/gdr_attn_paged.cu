@@ -30,7 +30,7 @@
 // per row splits exactly but for values 2^-17 below the row's largest.  The
 // key scales multiply the scores.  The value scales sv_j enter the
 // weights, w_j = 2^(a_j + log2 sv_j - m), which P holds, with the maximum taken
-// over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Four more warps split
+// over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Two more warps split
 // Q and prepare the scales.
 //
 // Every wait is bounded (2 s); on expiry a role records GDR_ERR_TIMEOUT, the
@@ -56,7 +56,9 @@ constexpr int KEYS = 128;  // keys per tile
 // Cost of starting and finishing an item, in tiles.
 constexpr int ITEM_COST = 2;
 constexpr int SOFTMAX_WARPS = 8;
-constexpr int W_LOAD = 8, W_MMA = 9, W_AUX = 10;  // warps 10 .. 13: code caches only
+constexpr int W_LOAD = 8, W_MMA = 9, W_AUX = 10;  // from W_AUX on: code caches only
+constexpr int AUX_WARPS = 2;  // 12 warps: 3 a scheduler, which leaves 168 registers a thread
+constexpr int NRAW = 4;       // tiles of key and value scales in flight
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // Unwinding after an expired wait: arrivals still owed come within microseconds
@@ -77,11 +79,12 @@ struct Layout {
     static constexpr uint32_t S_Q = 0;
     static constexpr uint32_t S_RING = 4 * BOX;
     static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;      // [2][2][128] floats
-    static constexpr uint32_t S_SCALE = S_RED + 2048;             // [2][3][128] floats
-    static constexpr uint32_t S_ROWK = S_SCALE + (E4M3 ? 3072 : 0);  // [2][128] floats
+    static constexpr uint32_t S_SCALE = S_RED + 2048;                // [2][3][128] floats
+    static constexpr uint32_t S_RAW = S_SCALE + (E4M3 ? 3072 : 0);   // [NRAW][2][128] floats
+    static constexpr uint32_t S_ROWK = S_RAW + (E4M3 ? NRAW * 1024 : 0);  // [2][128] floats
     static constexpr uint32_t S_BAR = S_ROWK + (E4M3 ? 1024 : 0);
     static constexpr uint32_t S_BYTES = S_BAR + 512;
-    static constexpr int THREADS = 32 * (E4M3 ? 14 : 10);
+    static constexpr int THREADS = 32 * (W_AUX + (E4M3 ? AUX_WARPS : 0));
 };
 static_assert(Layout<false>::S_BYTES <= 232448 && Layout<true>::S_BYTES <= 232448, "shared memory");
 
@@ -134,15 +137,17 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 // A sequence's lengths as the kernels use them.
 struct Seq {
     int cu0, q, len;  // first packed row, new tokens, tokens before; len -1: lengths not usable
-    __device__ __forceinline__ void load(const AttnParams &p, int s) {
-        const gdr_kv_pages &c = p.a.pages;
-        cu0 = __ldg(c.cu_seqlens + s);
-        const int end = min(__ldg(c.cu_seqlens + s + 1), (int)p.a.n_tok);
-        cu0 = max(cu0, 0);
-        q = max(end - cu0, 0);
-        len = __ldg(p.a.cache_len + s);
+    // From cu_seqlens[s], cu_seqlens[s + 1] and cache_len[s].
+    __device__ __forceinline__ void set(const AttnParams &p, int begin, int end, int before) {
+        cu0 = max(begin, 0);
+        q = max(min(end, (int)p.a.n_tok) - cu0, 0);
+        len = before;
         const int64_t total = (int64_t)len + q;
-        if (len < 0 || total > ((int64_t)c.table_width << p.shift) || total > 0x7fffff00LL) len = -1;
+        if (len < 0 || total > ((int64_t)p.a.pages.table_width << p.shift) || total > 0x7fffff00LL) len = -1;
+    }
+    __device__ __forceinline__ void load(const AttnParams &p, int s) {
+        const int32_t *cu = p.a.pages.cu_seqlens + s;
+        set(p, __ldg(cu), __ldg(cu + 1), __ldg(p.a.cache_len + s));
     }
     __device__ __forceinline__ int tiles(const AttnParams &p) const {
         return (q + p.tile_tok - 1) / p.tile_tok;
@@ -179,16 +184,24 @@ struct Item {
     int a, b;         // this CTA's tiles
 };
 
-// The items of a CTA's stretch, in order.  Every role walks them by itself.
+// The items of a CTA's stretch, in order.  Every role walks them by itself; the
+// lengths of the next sequence are fetched while one is walked.
 struct Walk {
     Plan w;
     Seq q;
     int n_tiles;
+    int next_end, next_len;  // of sequence w.s + 1
     __device__ __forceinline__ Walk(const AttnParams &p, const Plan *plan) : w(*plan), n_tiles(0) {
         if (w.u < w.hi) {
             q.load(p, w.s);
             n_tiles = q.tiles(p);
+            fetch(p);
         }
+    }
+    __device__ __forceinline__ void fetch(const AttnParams &p) {
+        const int s = min(w.s + 1, p.a.pages.n_seq - 1);
+        next_end = __ldg(p.a.pages.cu_seqlens + s + 1);
+        next_len = __ldg(p.a.cache_len + s);
     }
     __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
         const gdr_kv_pages &c = p.a.pages;
@@ -198,8 +211,9 @@ struct Walk {
                 if (n_tiles == 0 || ++w.g == c.H_kv) {
                     w.g = 0;
                     if (++w.s >= c.n_seq) return false;
-                    q.load(p, w.s);
+                    q.set(p, q.cu0 + q.q, next_end, next_len);
                     n_tiles = q.tiles(p);
+                    fetch(p);
                 }
             }
             const int first = w.i * p.tile_tok;
@@ -295,6 +309,31 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 // Two f16 values as e4m3 codes in two parts, the second what the first leaves.
 __device__ __forceinline__ void split2(uint32_t h2, uint16_t &hi, uint16_t &lo) {
     uint32_t back, rest;
@@ -302,6 +341,26 @@ __device__ __forceinline__ void split2(uint32_t h2, uint16_t &hi, uint16_t &lo) 
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h2), "r"(back));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
+}
+// Four weights as e4m3 codes in two parts, with integer instructions: the conversions
+// run at 16 lanes a clock for the SM, like the exponentials beside them.  The weights come
+// times 2^-8, below 2: there f16 has e4m3's exponents (2^-14 its smallest normal value,
+// where the codes' is 2^-6), so a code is an f16 value rounded to 3 bits of mantissa,
+// without its sign's neighbour bit, which is 0.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo) {
+    const uint32_t y[2] = {f16x2(a, b), f16x2(c, d)};
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = y[i] + 0x00400040u;  // weights are positive: round by a carry
+        uint32_t rest;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y[i]), "r"(t & 0xff80ff80u));
+        h[i] = t << 1;
+        rest += 0x00400040u;  // away from zero, whatever the sign
+        l[i] = ((rest << 1) & 0x7fff7fffu) | (rest & 0x80008000u);
+    }
+    hi = __byte_perm(h[0], h[1], 0x7531);
+    lo = __byte_perm(l[0], l[1], 0x7531);
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
     uint4 v;
@@ -331,19 +390,21 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::S_BAR);  // [NSLOT] slot landed
     uint64_t *empty = full + NSLOT;    // [NSLOT] slot consumed
     uint64_t *q_full = empty + NSLOT;  // Q tile landed
-    uint64_t *q_split = q_full + 1;    // Q tile split in hi and lo (4 warps)
+    uint64_t *q_split = q_full + 1;    // Q tile split in hi and lo (aux warps)
     uint64_t *q_free = q_full + 2;     // the item's S products are done
     uint64_t *bar_s = q_full + 3;      // [2] S of a tile in TMEM
     uint64_t *bar_p = q_full + 5;      // [2] P of a tile in TMEM, O rescaled (8 warps)
     uint64_t *bar_o = q_full + 7;      // [2] O += P V of a tile done
     uint64_t *o_free = q_full + 9;     // the item's O has been read (8 warps)
-    uint64_t *sc_full = q_full + 10;   // [2] scales of a tile prepared (4 warps)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::S_BAR + 256);
-    Plan *plan = reinterpret_cast<Plan *>(sm + L::S_BAR + 272);
-    int64_t *warp_sum = reinterpret_cast<int64_t *>(sm + L::S_BAR + 320);  // [14]
+    uint64_t *sc_full = q_full + 10;   // [2] scales of a tile prepared (aux warps)
+    uint64_t *raw_full = q_full + 12;  // [NRAW] scales of a tile landed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::S_BAR + 288);
+    Plan *plan = reinterpret_cast<Plan *>(sm + L::S_BAR + 304);
+    int64_t *warp_sum = reinterpret_cast<int64_t *>(sm + L::S_BAR + 352);  // one a warp
     float *red = reinterpret_cast<float *>(sm + L::S_RED);
     const gdr_kv_pages &c = p.a.pages;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (Through a shuffle, so that the compiler knows the warp's number to be uniform.)
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
     const uint32_t sbase = smem_u32(sm);
     const uint32_t ring = sbase + L::S_RING, sq = sbase + L::S_Q;
 
@@ -354,14 +415,15 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             mbar_init(empty + i, 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_split, 4);
+        mbar_init(q_split, AUX_WARPS);
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + i, 1);
             mbar_init(bar_p + i, SOFTMAX_WARPS);
             mbar_init(bar_o + i, 1);
-            mbar_init(sc_full + i, 4);
+            mbar_init(sc_full + i, AUX_WARPS);
         }
+        for (int i = 0; i < NRAW; ++i) mbar_init(raw_full + i, 1);
         mbar_init(o_free, SOFTMAX_WARPS);
         mbar_fence_init();
     }
@@ -390,7 +452,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         // ---------------------------------------------------------- loads
         // Lane 0 keeps the barriers; every lane issues its boxes of a slot.
         bool ok = true, bad = false;
-        int n_use = 0, n_item = 0;
+        int n_use = 0, n_item = 0, n_raw = 0;
         if (lane == 0) {
             tma_prefetch_map(&p.tm_q);
             tma_prefetch_map(&p.tm_k);
@@ -439,6 +501,23 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         tma_load_2d(ring + (use % NSLOT) * L::SLOT + col * BOX + part * kr * 128,
                                     &p.tm_k, h * 128 + col * 64, r, bar);
                     n_use = use + 1;
+                }
+                if constexpr (E4M3) {
+                    // The tile's scales: lanes 0 .. 7 the keys', 8 .. 15 the values', a part
+                    // of kr rows each; none for a page that does not exist.  The stage is
+                    // free: its tile's weights were multiplied before K's slot came free.
+                    const int part = lane & 7;
+                    const int r = __shfl_sync(kFullMask, row, (part * (kr >> 4)) & 7);
+                    const bool has = lane < 16 && part < parts && r < p.n_rows;
+                    const uint32_t bytes = (uint32_t)kr * 4;
+                    const int n_copy = __popc(__ballot_sync(kFullMask, has));
+                    uint64_t *bar = raw_full + n_raw % NRAW;
+                    if (lane == 0) bulk_expect(bar, bytes * n_copy);
+                    __syncwarp();
+                    if (has)
+                        bulk_copy(sm + L::S_RAW + (n_raw % NRAW) * 1024 + (lane >> 3) * 512 + part * bytes,
+                                  (lane < 8 ? c.k_scale : c.v_scale) + r, bytes, bar);
+                    ++n_raw;
                 }
             };
             auto load_v = [&](int j, int use0, int row) {
@@ -495,6 +574,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 // No copy may land after the CTA ends.
                 if (n_item > 0) mbar_wait(q_full, (uint32_t)(n_item - 1) & 1u, kWaitNs);
                 for (int u = max(0, n_use - NSLOT); u < n_use; ++u) full_wait(u);
+                for (int u = max(0, n_raw - NRAW); u < n_raw; ++u)
+                    mbar_wait(raw_full + u % NRAW, (uint32_t)(u / NRAW) & 1u, kWaitNs);
             }
             // Nor may an arrival that a commit owes: the last use of every slot, the
             // last item's Q.
@@ -506,67 +587,82 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         __syncwarp();
     } else if (warp == W_MMA) {
         // ------------------------------------------------------ MMA issue
-        if (lane == 0) {
+        // One elected thread.  Descriptors are a base per operand plus a constant step:
+        // what is left to compute per instruction is one addition.
+        if (elect_one()) {
             constexpr Kind KIND = E4M3 ? Kind::E4M3 : Kind::BF16;
             constexpr uint32_t ID_S = instr_desc<KIND>(128, KEYS, false, false);
             constexpr uint32_t ID_O = instr_desc<KIND>(128, E4M3 ? 128 : 256, false, true);
+            constexpr int STEP = E4M3 ? 32 : 16;  // keys per instruction of P V
+            const uint64_t dq = smem_desc_sw128(sq, 16, 1024);
+            const uint64_t dk = smem_desc_sw128(ring, 16, 1024);
+            const uint64_t dv = smem_desc_sw128(ring, E4M3 ? BOX : BOX / 2, 1024);
             bool ok = true;
             int jt = 0, base = 0, n_item = 0;
+            // S of tile `tile`, from the ring's uses u, u + 1.
+            auto score = [&](int tile, int u) {
+                const uint32_t d = tm + TM_S + 128 * (tile & 1);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!full_wait(u + h)) return false;
+                    fence_after_sync();
+                    const uint64_t b = dk + (uint64_t)((u + h) % NSLOT) * (L::SLOT >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        // bf16: box k / 4 of the half; e4m3: the hi, then the lo part
+                        mma<KIND>(d, dq + ((2 * h + (k >> 2)) * (BOX >> 4) + (k & 3) * 2),
+                                  b + ((E4M3 ? 0 : (k >> 2) * (BOX >> 4)) + (k & 3) * 2), ID_S,
+                                  (h | k) ? 1u : 0u);
+                }
+                commit(smem_u32(bar_s + (tile & 1)));
+                commit(smem_u32(empty + u % NSLOT));
+                commit(smem_u32(empty + (u + 1) % NSLOT));
+                return true;
+            };
+            // O (+)= P V of half h of a tile: `steps` instructions, twice (hi, lo) for codes.
+            auto weigh = [&](uint32_t pt, int u, int h, int steps, uint32_t more) {
+                const uint64_t b = dv + (uint64_t)(u % NSLOT) * (L::SLOT >> 4);
+                if constexpr (!E4M3) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < steps)
+                            mma_ta(tm + TM_O, pt + 64 * h + 8 * k, b + k * (2048 >> 4), ID_O,
+                                   (h | k) ? 1u : more);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int part = x >> 2, k = x & 3;
+                        if (k < steps)
+                            mma_ta_e4m3(tm + TM_O + 128 * h, pt + 64 * (k >> 1) + 16 * part + 8 * (k & 1),
+                                        b + k * (4096 >> 4), ID_O, x ? 1u : more);
+                    }
+                }
+            };
             while (ok && walk.next(p, it)) {
                 if (it.n_kv == 0) continue;
                 const int n = it.b - it.a;
-                ok = mbar_wait(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u, kWaitNs);
-                auto score = [&](int i) {  // S of the item's tile i
-                    const uint32_t d = tm + TM_S + 128 * ((jt + i) & 1);
-                    const int u0 = base + use_k(i);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!full_wait(u0 + h)) return false;
-                        fence_after_sync();
-                        const uint32_t kb = ring + ((u0 + h) % NSLOT) * L::SLOT;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            // bf16: box k / 4 of the half; e4m3: the hi, then the lo part
-                            const uint32_t qa = sq + (2 * h + (k >> 2)) * BOX + (k & 3) * 32;
-                            const uint32_t ka = kb + (E4M3 ? 0 : (k >> 2) * BOX) + (k & 3) * 32;
-                            mma<KIND>(d, smem_desc_sw128(qa, 16, 1024), smem_desc_sw128(ka, 16, 1024),
-                                      ID_S, (h | k) ? 1u : 0u);
-                        }
-                    }
-                    commit(smem_u32(bar_s + ((jt + i) & 1)));
-                    commit(smem_u32(empty + u0 % NSLOT));
-                    commit(smem_u32(empty + (u0 + 1) % NSLOT));
-                    if (i == n - 1) commit(smem_u32(q_free));
-                    return true;
-                };
-                ok = ok && score(0);
+                ok = mbar_wait(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u, kWaitNs) &&
+                     score(jt, base + use_k(0));
+                if (n == 1 && ok) commit(smem_u32(q_free));
                 for (int i = 0; i < n && ok; ++i) {
-                    if (i + 1 < n) ok = score(i + 1);
+                    if (i + 1 < n) {
+                        ok = score(jt + i + 1, base + use_k(i + 1));
+                        if (i + 2 == n && ok) commit(smem_u32(q_free));
+                    }
                     if (ok && i == 0 && n_item > 0) ok = mbar_wait(o_free, (uint32_t)(n_item - 1) & 1u, kWaitNs);
                     const int j = jt + i, u0 = base + use_v(i, n);
                     ok = ok && mbar_wait(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
                     const int keys = min(KEYS, it.end - (it.a + i) * KEYS);
                     const uint32_t pt = tm + TM_S + 128 * (j & 1);
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = full_wait(u0 + h);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && full_wait(u0 + h);
                         if (!ok) break;
                         fence_after_sync();
-                        const uint32_t vb = ring + ((u0 + h) % NSLOT) * L::SLOT;
-                        if constexpr (!E4M3) {
-                            const int steps = min(4, (keys - 64 * h + 15) >> 4);
-                            for (int k = 0; k < steps; ++k)
-                                mma_ta(tm + TM_O, pt + 64 * h + 8 * k,
-                                       smem_desc_sw128(vb + k * 2048, BOX / 2, 1024), ID_O,
-                                       (i | h | k) ? 1u : 0u);
-                        } else {
-                            const int steps = (keys + 31) >> 5;
-                            for (int part = 0; part < 2; ++part)
-                                for (int k = 0; k < steps; ++k)
-                                    mma_ta_e4m3(tm + TM_O + 128 * h,
-                                                pt + 64 * (k >> 1) + 16 * part + 8 * (k & 1),
-                                                smem_desc_sw128(vb + k * 4096, BOX, 1024), ID_O,
-                                                (i | part | k) ? 1u : 0u);
-                        }
+                        if (keys == KEYS)
+                            weigh(pt, u0 + h, h, 4, i ? 1u : 0u);
+                        else  // bf16: a slot holds 64 of the keys
+                            weigh(pt, u0 + h, h, ((E4M3 ? keys : keys - 64 * h) + STEP - 1) / STEP, i ? 1u : 0u);
                     }
                     if (!ok) break;
                     commit(smem_u32(bar_o + (j & 1)));
@@ -582,8 +678,10 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         __syncwarp();
     } else if (E4M3 && warp >= W_AUX) {
         // -------------------------------------- Q in two parts, and the scales
-        const int t = tid - 32 * W_AUX;  // row of Q, key of a tile
+        const int t = tid - 32 * W_AUX;
+        constexpr int NT = 32 * AUX_WARPS;
         float *scales = reinterpret_cast<float *>(sm + L::S_SCALE);
+        const float *raw = reinterpret_cast<const float *>(sm + L::S_RAW);
         float *rowk = reinterpret_cast<float *>(sm + L::S_ROWK);
         bool ok = true;
         int jt = 0, n_item = 0;
@@ -591,82 +689,72 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (it.n_kv == 0) continue;
             ok = __all_sync(kFullMask, mbar_wait(q_full, (uint32_t)n_item & 1u, kWaitNs));
             if (!ok) break;
-            // Row t: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (t % 8).
-            const uint32_t row = sq + t * 128;
-            auto chunk = [&](int b, int j) { return row + b * BOX + ((j ^ (t & 7)) << 4); };
-            uint32_t top = 0;  // largest magnitude, as bf16 bits
+            // Row r: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (r % 8).
+            for (int r = t; r < it.n_tok * p.n_rep; r += NT) {
+                const uint32_t row = sq + r * 128;
+                auto chunk = [&](int b, int j) { return row + b * BOX + ((j ^ (r & 7)) << 4); };
+                uint32_t top = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < 4; ++b)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint4 v = ld_shared16(chunk(b, j));
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                }
-            // A power of two that takes the largest value into [128, 256).
-            const int e = min(max((int)max(top >> 16, top & 0xffffu) >> 7, 8), 254);
-            const float up = __uint_as_float((uint32_t)(261 - e) << 23);
-            rowk[(n_item & 1) * ROWS + t] = __uint_as_float((uint32_t)(e - 7) << 23);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint4 x[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = ld_shared16(chunk(2 * h + (j >> 3), j & 7));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {  // 16 values
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint4 v = x[2 * j + (w >> 1)];
-                        const uint32_t v0 = w & 1 ? v.z : v.x, v1 = w & 1 ? v.w : v.y;
-                        uint16_t h0, h1, l0, l1;
-                        split2(f16x2(__uint_as_float(v0 << 16) * up,
-                                     __uint_as_float(v0 & 0xffff0000u) * up), h0, l0);
-                        split2(f16x2(__uint_as_float(v1 << 16) * up,
-                                     __uint_as_float(v1 & 0xffff0000u) * up), h1, l1);
-                        hi[w] = h0 | (uint32_t)h1 << 16;
-                        lo[w] = l0 | (uint32_t)l1 << 16;
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = ld_shared16(chunk(b, j));
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
                     }
-                    st_shared16(chunk(2 * h, j), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    st_shared16(chunk(2 * h + 1, j), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                // A power of two that takes the largest value into [128, 256).
+                const int e = min(max((int)max(top >> 16, top & 0xffffu) >> 7, 8), 254);
+                const float up = __uint_as_float((uint32_t)(261 - e) << 23);
+                rowk[(n_item & 1) * ROWS + r] = __uint_as_float((uint32_t)(e - 7) << 23);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint4 x[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = ld_shared16(chunk(2 * h + (j >> 3), j & 7));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {  // 16 values
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint4 v = x[2 * j + (w >> 1)];
+                            const uint32_t v0 = w & 1 ? v.z : v.x, v1 = w & 1 ? v.w : v.y;
+                            uint16_t h0, h1, l0, l1;
+                            split2(f16x2(__uint_as_float(v0 << 16) * up,
+                                         __uint_as_float(v0 & 0xffff0000u) * up), h0, l0);
+                            split2(f16x2(__uint_as_float(v1 << 16) * up,
+                                         __uint_as_float(v1 & 0xffff0000u) * up), h1, l1);
+                            hi[w] = h0 | (uint32_t)h1 << 16;
+                            lo[w] = l0 | (uint32_t)l1 << 16;
+                        }
+                        st_shared16(chunk(2 * h, j), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        st_shared16(chunk(2 * h + 1, j), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    }
                 }
             }
             fence_smem_to_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_split);
-            // Scales of key t of each tile, fetched a tile ahead.
-            auto fetch = [&](int j, float &ks, float &vs) {
-                const int key = j * KEYS + t;
-                ks = vs = 0.f;
-                if (j < it.b && key < it.end) {
-                    const int r = cache_row(c, p.shift, it.s, it.g, key);
-                    if (r >= 0) {
-                        ks = __ldg(c.k_scale + r);
-                        vs = __ldg(c.v_scale + r);
-                    }
-                }
-            };
-            float ks, vs;
-            fetch(it.a, ks, vs);
             for (int j = it.a; j < it.b; ++j, ++jt) {
-                float ks1, vs1;
-                fetch(j + 1, ks1, vs1);
+                ok = mbar_wait(raw_full + jt % NRAW, (uint32_t)(jt / NRAW) & 1u, kWaitNs);
                 // The stage was read by the softmax two tiles back.
-                if (jt >= 2)
-                    ok = __all_sync(kFullMask,
-                                    mbar_wait(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs));
+                if (jt >= 2) ok = ok && mbar_wait(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs);
+                ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 float *st = scales + (jt & 1) * 3 * KEYS;
-                // The smallest scale that an append writes stands for zero too: it keeps
-                // the key in the softmax's sum.
-                vs = fmaxf(vs, kScaleMin);
-                st[t] = ks * p.scale_log2;
-                st[KEYS + t] = log2f(vs);
-                st[2 * KEYS + t] = 1.f / vs;
+                const float *from = raw + (jt % NRAW) * 2 * KEYS;
+#pragma unroll
+                for (int x = t; x < KEYS; x += NT) {
+                    const bool in = j * KEYS + x < it.end;
+                    // The smallest scale that an append writes stands for zero too: it keeps
+                    // the key in the softmax's sum.  Keys past the end: any finite value.
+                    const float ks = in ? from[x] : 0.f;
+                    const float vs = in ? fmaxf(from[KEYS + x], kScaleMin) : 1.f;
+                    st[x] = ks * p.scale_log2;
+                    st[KEYS + x] = log2f(vs);
+                    st[2 * KEYS + x] = 1.f / vs;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_full + (jt & 1));
-                ks = ks1;
-                vs = vs1;
             }
             ++n_item;
         }
@@ -684,6 +772,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         // and may grow by 2^2.
         constexpr float kLazy = E4M3 ? 2.f : 8.f;
         constexpr float kUp = E4M3 ? 6.f : 0.f;
+        constexpr float kShift = E4M3 ? 8.f : 0.f;  // split4 takes weights times 2^-8
         const int half = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
         const int tok = r / p.n_rep, h = r - tok * p.n_rep;
@@ -728,17 +817,23 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         if (i == 0) row_factor = rowk[(n_item & 1) * ROWS + r];
                         const float4 *sk = reinterpret_cast<const float4 *>(scales + (j & 1) * 3 * KEYS + 64 * half);
                         const float4 *lv = sk + KEYS / 4;
+                        const float2 rf = make_float2(row_factor, row_factor);
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const float4 a = sk[x], b = lv[x];
-                            s[4 * x] = fmaf(s[4 * x] * row_factor, a.x, b.x);
-                            s[4 * x + 1] = fmaf(s[4 * x + 1] * row_factor, a.y, b.y);
-                            s[4 * x + 2] = fmaf(s[4 * x + 2] * row_factor, a.z, b.z);
-                            s[4 * x + 3] = fmaf(s[4 * x + 3] * row_factor, a.w, b.w);
+                            const float2 u = fma2(mul2(make_float2(s[4 * x], s[4 * x + 1]), rf),
+                                                  make_float2(a.x, a.y), make_float2(b.x, b.y));
+                            const float2 v = fma2(mul2(make_float2(s[4 * x + 2], s[4 * x + 3]), rf),
+                                                  make_float2(a.z, a.w), make_float2(b.z, b.w));
+                            s[4 * x] = u.x;
+                            s[4 * x + 1] = u.y;
+                            s[4 * x + 2] = v.x;
+                            s[4 * x + 3] = v.y;
                         }
                     }
-                    // Keys this row attends, of this thread's 64.
-                    const int lim = (mine ? it.pos0 + tok + 1 - k0 : 0) - 64 * half;
+                    // Keys this row attends, of this thread's 64 (a row that does not exist:
+                    // all of them, whatever they are).
+                    const int lim = mine ? it.pos0 + tok + 1 - k0 - 64 * half : 64;
                     if (__any_sync(kFullMask, lim < 64)) {
 #pragma unroll
                         for (int x = 0; x < 64; ++x)
@@ -767,37 +862,38 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     l *= alpha;
                     const bool rescale = __any_sync(kFullMask, moves) && i > 0;
                     // -inf (nothing attended yet) as 0: every exponent below is -inf then.
-                    const float sub = (m_ref == -INFINITY ? 0.f : m_ref) - kUp;
+                    const float sub = (m_ref == -INFINITY ? 0.f : m_ref) - kUp + kShift;
                     uint32_t pk[32];
-                    float l2[2] = {0.f, 0.f};
+                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+                    const float2 sub2 = make_float2(-sub, -sub);
                     if constexpr (!E4M3) {
+                        const float2 cl = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const float a = exp2_fast(fmaf(s[2 * x], p.scale_log2, -sub));
-                            const float b = exp2_fast(fmaf(s[2 * x + 1], p.scale_log2, -sub));
-                            l2[0] += a;
-                            l2[1] += b;
-                            pk[x] = bf16x2(a, b);
+                        for (int x = 0; x < 32; x += 2) {
+                            const float2 u = fma2(make_float2(s[2 * x], s[2 * x + 1]), cl, sub2);
+                            const float2 v = fma2(make_float2(s[2 * x + 2], s[2 * x + 3]), cl, sub2);
+                            const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                            const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                            l2 = add2(l2, a);
+                            l3 = add2(l3, b);
+                            pk[x] = bf16x2(a.x, a.y);
+                            pk[x + 1] = bf16x2(b.x, b.y);
                         }
                     } else {
                         const float4 *rs = reinterpret_cast<const float4 *>(scales + ((j & 1) * 3 + 2) * KEYS + 64 * half);
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const float4 f = rs[x];
-                            const float a = exp2_fast(s[4 * x] - sub), b = exp2_fast(s[4 * x + 1] - sub);
-                            const float d = exp2_fast(s[4 * x + 2] - sub), e = exp2_fast(s[4 * x + 3] - sub);
-                            l2[0] = fmaf(a, f.x, l2[0]);
-                            l2[1] = fmaf(b, f.y, l2[1]);
-                            l2[0] = fmaf(d, f.z, l2[0]);
-                            l2[1] = fmaf(e, f.w, l2[1]);
-                            uint16_t h0, h1, l0, l1;
-                            split2(f16x2(a, b), h0, l0);
-                            split2(f16x2(d, e), h1, l1);
-                            pk[x] = h0 | (uint32_t)h1 << 16;
-                            pk[16 + x] = l0 | (uint32_t)l1 << 16;
+                            const float2 u = add2(make_float2(s[4 * x], s[4 * x + 1]), sub2);
+                            const float2 v = add2(make_float2(s[4 * x + 2], s[4 * x + 3]), sub2);
+                            const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                            const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                            l2 = fma2(a, make_float2(f.x, f.y), l2);
+                            l3 = fma2(b, make_float2(f.z, f.w), l3);
+                            split4(a.x, a.y, b.x, b.y, pk[x], pk[16 + x]);
                         }
                     }
-                    l += l2[0] + l2[1];
+                    l += (l2.x + l2.y) + (l3.x + l3.y);
                     // Over S: both warps of the rows have read it (the barrier above).
                     {
                         float pf[32];
@@ -855,18 +951,26 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             base += 4 * n;
             ++n_item;
             // The item's end: the row's sum over both threads, then O.
+            l *= E4M3 ? 256.f : 1.f;  // 2^kShift
             red[((jt & 1) * 2 + half) * ROWS + r] = l;
+            const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
+            uint4 gate[16];  // the row's gates, fetched while the last product runs
+            if (whole && mine && p.a.gate) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + 128 * half);
+#pragma unroll
+                for (int x = 0; x < 16; ++x) gate[x] = __ldg(src + x);
+            }
             const bool ok = wait_o(jt - 1, kWaitNs);
             dead = group_sync_or(1 + quad, 64, !ok || fault);
             if (dead) break;
             l += red[((jt & 1) * 2 + (half ^ 1)) * ROWS + r];
             group_sync_or(1 + quad, 64, false);  // the next tile writes there
             fence_after_sync();
-            const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (some) {
-#pragma unroll 1
+#pragma unroll
                 for (int x = 0; x < 128; x += 32) {
                     float o[32];
                     __syncwarp();
@@ -880,17 +984,14 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                             *reinterpret_cast<float4 *>(po + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
                         continue;
                     }
-                    const __nv_bfloat16 *gate =
-                        p.a.gate ? static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + d0
-                                 : nullptr;
                     const int64_t at = grow * p.a.out_stride + gh * D + d0;
 #pragma unroll
                     for (int y = 0; y < 32; y += 8) {
                         float v[8];
 #pragma unroll
                         for (int z = 0; z < 8; ++z) v[z] = o[y + z] * inv;
-                        if (gate) {
-                            const uint4 g8 = __ldg(reinterpret_cast<const uint4 *>(gate + y));
+                        if (p.a.gate) {
+                            const uint4 g8 = gate[(x + y) >> 3];
                             const uint32_t gw[4] = {g8.x, g8.y, g8.z, g8.w};
 #pragma unroll
                             for (int z = 0; z < 8; ++z) {

@@ -123,6 +123,15 @@ __device__ __forceinline__ void gemm_ta(uint32_t d, uint32_t a_tmem, uint32_t b,
                (acc || kk > 0) ? 1u : 0u);
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Arrive on an mbarrier once all tcgen05 work issued so far by this thread is done.
 __device__ __forceinline__ void commit(uint32_t mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

@@ -98,7 +98,7 @@ PAGES = [
     ("negative_width", dict(table_width=-1), INVALID),
     ("reserved_pages", {}, INVALID),
     ("misaligned_pages", dict(v=FAKE + 8), MISALIGNED),
-    ("misaligned_scale", dict(k_scale=FAKE + 2), MISALIGNED),
+    ("misaligned_scale", dict(k_scale=FAKE + 8), MISALIGNED),
     ("misaligned_table", dict(page_table=FAKE + 1), MISALIGNED),
     ("misaligned_cu", dict(cu_seqlens=FAKE + 2), MISALIGNED),
     ("negative_tokens", dict(n_tok=-1), INVALID),
