@@ -19,8 +19,8 @@
 // In a CTA, one warp streams K and V through a ring of shared-memory slots with
 // TMA tensor copies, page by page, into 128-byte-swizzled tiles; one thread
 // issues S = Q K^T (M = 128 rows, N = 128 keys, K = 256) and O += P V (N = 256)
-// on tcgen05 with S (two buffers) and O in tensor memory; eight softmax warps
-// (thread = row, two threads a row, 64 keys each) keep the running maximum and
+// on tcgen05 with S (two buffers) and O in tensor memory; the softmax warps
+// (thread = row, two threads a row, four for codes) keep the running maximum and
 // sum, write P over S in tensor memory and rescale O when the maximum has moved
 // far.  S of the next tile is computed while the softmax works on this one.
 //
@@ -55,9 +55,7 @@ constexpr int ROWS = 128;  // query rows per item
 constexpr int KEYS = 128;  // keys per tile
 // Cost of starting and finishing an item, in tiles.
 constexpr int ITEM_COST = 2;
-constexpr int SOFTMAX_WARPS = 8;
-constexpr int W_LOAD = 8, W_MMA = 9, W_AUX = 10;  // from W_AUX on: code caches only
-constexpr int AUX_WARPS = 2;  // 12 warps: 3 a scheduler, which leaves 168 registers a thread
+constexpr int AUX_WARPS = 2;  // split Q, prepare scales: code caches only
 constexpr int NRAW = 4;       // tiles of key and value scales in flight
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -76,14 +74,18 @@ struct Layout {
     // [64 keys][64 dims]).  e4m3: both are halves of the dims ([128 keys][128 dims]).
     static constexpr uint32_t SLOT = E4M3 ? BOX : 2 * BOX;
     static constexpr int NSLOT = E4M3 ? 9 : 5;
+    // Threads that share a row, each with KEYS / PARTS keys of a tile.
+    static constexpr int PARTS = E4M3 ? 4 : 2;
+    static constexpr int SOFTMAX = 4 * PARTS;  // softmax warps: 0 ..
+    static constexpr int W_LOAD = SOFTMAX, W_MMA = SOFTMAX + 1, W_AUX = SOFTMAX + 2;
     static constexpr uint32_t S_Q = 0;
     static constexpr uint32_t S_RING = 4 * BOX;
-    static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;      // [2][2][128] floats
-    static constexpr uint32_t S_SCALE = S_RED + 2048;                // [2][3][128] floats
+    static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;         // [2][PARTS][128] floats
+    static constexpr uint32_t S_SCALE = S_RED + 1024 * PARTS;        // [2][3][128] floats
     static constexpr uint32_t S_RAW = S_SCALE + (E4M3 ? 3072 : 0);   // [NRAW][2][128] floats
     static constexpr uint32_t S_ROWK = S_RAW + (E4M3 ? NRAW * 1024 : 0);  // [2][128] floats
     static constexpr uint32_t S_BAR = S_ROWK + (E4M3 ? 1024 : 0);
-    static constexpr uint32_t S_BYTES = S_BAR + 512;
+    static constexpr uint32_t S_BYTES = S_BAR + 544;
     static constexpr int THREADS = 32 * (W_AUX + (E4M3 ? AUX_WARPS : 0));
 };
 static_assert(Layout<false>::S_BYTES <= 232448 && Layout<true>::S_BYTES <= 232448, "shared memory");
@@ -108,7 +110,7 @@ struct AttnParams {
     int *status;      // workspace
     Desc *desc;       // [CTAs]
     float *part_ml;   // [2 CTAs][128][2]: maximum (log2) and sum
-    float *part_o;    // [2 CTAs][128][256]
+    float *part_o;    // [2 CTAs][64][128][4]: dims 4c .. of row r at [c][r], so that lanes = rows store together
 };
 
 // sum_{i < n} floor((a i + b) / m), in the steps of Euclid's algorithm.
@@ -294,6 +296,24 @@ __device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Pla
     __syncthreads();
 }
 
+// Waits for a barrier's phase, at most `limit` ns.  The first look is inline, the rest a
+// call: a CTA's five roles share the instruction cache, and code that is repeated at every wait
+// costs more there than the call.
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, uint64_t limit) {
+    return mbar_wait(bar, parity, limit);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint64_t limit = kWaitNs) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done || wait_on(bar, parity, limit);
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -356,8 +376,8 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
         uint32_t rest;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y[i]), "r"(t & 0xff80ff80u));
         h[i] = t << 1;
-        rest += 0x00400040u;  // away from zero, whatever the sign
-        l[i] = ((rest << 1) & 0x7fff7fffu) | (rest & 0x80008000u);
+        // Rounded away from zero, whatever the sign, and shifted past it.
+        l[i] = ((rest * 2 + 0x00800080u) & 0x7fff7fffu) | (rest & 0x80008000u);
     }
     hi = __byte_perm(h[0], h[1], 0x7531);
     lo = __byte_perm(l[0], l[1], 0x7531);
@@ -376,6 +396,24 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
                  : "memory");
 }
 
+// Four 16-byte chunks in each of four neighbouring lanes, transposed: chunk k of lane l
+// goes to chunk l of lane k (its own inverse).
+__device__ __forceinline__ void swap_chunk(uint4 &a, uint4 &b, bool upper, int lanes) {
+    uint4 send = upper ? a : b;
+    send.x = __shfl_xor_sync(kFullMask, send.x, lanes);
+    send.y = __shfl_xor_sync(kFullMask, send.y, lanes);
+    send.z = __shfl_xor_sync(kFullMask, send.z, lanes);
+    send.w = __shfl_xor_sync(kFullMask, send.w, lanes);
+    if (upper) a = send;
+    else b = send;
+}
+__device__ __forceinline__ void transpose4(uint4 (&c)[4], int lane) {
+    swap_chunk(c[0], c[1], lane & 1, 1);
+    swap_chunk(c[2], c[3], lane & 1, 1);
+    swap_chunk(c[0], c[2], lane & 2, 2);
+    swap_chunk(c[1], c[3], lane & 2, 2);
+}
+
 // Uses of the ring by an item of n tiles, 4 a tile, in the order the MMA thread takes
 // them: K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ int use_k(int i) { return i == 0 ? 0 : 4 * i - 2; }
@@ -385,7 +423,7 @@ template <bool E4M3, bool OUT_BF16>
 __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ AttnParams p) {
     using L = Layout<E4M3>;
-    constexpr int NSLOT = L::NSLOT;
+    constexpr int NSLOT = L::NSLOT, PARTS = L::PARTS;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::S_BAR);  // [NSLOT] slot landed
     uint64_t *empty = full + NSLOT;    // [NSLOT] slot consumed
@@ -419,12 +457,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + i, 1);
-            mbar_init(bar_p + i, SOFTMAX_WARPS);
+            mbar_init(bar_p + i, L::SOFTMAX);
             mbar_init(bar_o + i, 1);
             mbar_init(sc_full + i, AUX_WARPS);
         }
         for (int i = 0; i < NRAW; ++i) mbar_init(raw_full + i, 1);
-        mbar_init(o_free, SOFTMAX_WARPS);
+        mbar_init(o_free, L::SOFTMAX);
         mbar_fence_init();
     }
     wait_for_predecessor();
@@ -438,7 +476,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     const uint32_t tm = *tmem_slot;
     auto report = [&](int status) { atomicMax(&desc->status, status); };
     auto full_wait = [&](int use) {
-        return mbar_wait(full + use % NSLOT, (uint32_t)(use / NSLOT) & 1u, kWaitNs);
+        return wait_bar(full + use % NSLOT, (uint32_t)(use / NSLOT) & 1u);
     };
     // The swizzled tiles must start on 1024-byte boundaries.
     const bool usable = (sbase & 1023u) == 0;
@@ -448,7 +486,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     Item it;
     if (!usable) {
         // nothing runs
-    } else if (warp == W_LOAD) {
+    } else if (warp == L::W_LOAD) {
         // ---------------------------------------------------------- loads
         // Lane 0 keeps the barriers; every lane issues its boxes of a slot.
         bool ok = true, bad = false;
@@ -481,7 +519,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             // One slot: n_box rows of boxes with n_col boxes each.
             auto acquire = [&](int use) {
                 if (use >= NSLOT && lane == 0)
-                    ok = mbar_wait(empty + use % NSLOT, (uint32_t)(use / NSLOT - 1) & 1u, kWaitNs);
+                    ok = wait_bar(empty + use % NSLOT, (uint32_t)(use / NSLOT - 1) & 1u);
                 ok = __shfl_sync(kFullMask, ok, 0);
                 return ok;
             };
@@ -546,7 +584,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             const int n = it.b - it.a, base = n_use;
             int row = page_row(it.a), row1 = page_row(it.a + 1);
             if (n_item > 0) {
-                if (lane == 0) ok = mbar_wait(q_free, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                if (lane == 0) ok = wait_bar(q_free, (uint32_t)(n_item - 1) & 1u);
                 ok = __shfl_sync(kFullMask, ok, 0);
                 if (!ok) break;
             }
@@ -572,20 +610,20 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (!ok) {
                 report(kTimeout);
                 // No copy may land after the CTA ends.
-                if (n_item > 0) mbar_wait(q_full, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                if (n_item > 0) wait_bar(q_full, (uint32_t)(n_item - 1) & 1u);
                 for (int u = max(0, n_use - NSLOT); u < n_use; ++u) full_wait(u);
                 for (int u = max(0, n_raw - NRAW); u < n_raw; ++u)
-                    mbar_wait(raw_full + u % NRAW, (uint32_t)(u / NRAW) & 1u, kWaitNs);
+                    wait_bar(raw_full + u % NRAW, (uint32_t)(u / NRAW) & 1u);
             }
             // Nor may an arrival that a commit owes: the last use of every slot, the
             // last item's Q.
             const uint64_t lim = ok ? kWaitNs : kDrainNs;
             for (int u = max(0, n_use - NSLOT); u < n_use; ++u)
-                mbar_wait(empty + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, lim);
-            if (n_item > 0) mbar_wait(q_free, (uint32_t)(n_item - 1) & 1u, lim);
+                wait_bar(empty + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, lim);
+            if (n_item > 0) wait_bar(q_free, (uint32_t)(n_item - 1) & 1u, lim);
         }
         __syncwarp();
-    } else if (warp == W_MMA) {
+    } else if (warp == L::W_MMA) {
         // ------------------------------------------------------ MMA issue
         // One elected thread.  Descriptors are a base per operand plus a constant step:
         // what is left to compute per instruction is one addition.
@@ -602,17 +640,18 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             // S of tile `tile`, from the ring's uses u, u + 1.
             auto score = [&](int tile, int u) {
                 const uint32_t d = tm + TM_S + 128 * (tile & 1);
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     if (!full_wait(u + h)) return false;
                     fence_after_sync();
+                    const uint64_t a = dq + (uint64_t)h * (2 * BOX >> 4);
                     const uint64_t b = dk + (uint64_t)((u + h) % NSLOT) * (L::SLOT >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         // bf16: box k / 4 of the half; e4m3: the hi, then the lo part
-                        mma<KIND>(d, dq + ((2 * h + (k >> 2)) * (BOX >> 4) + (k & 3) * 2),
+                        mma<KIND>(d, a + ((k >> 2) * (BOX >> 4) + (k & 3) * 2),
                                   b + ((E4M3 ? 0 : (k >> 2) * (BOX >> 4)) + (k & 3) * 2), ID_S,
-                                  (h | k) ? 1u : 0u);
+                                  k ? 1u : (uint32_t)h);
                 }
                 commit(smem_u32(bar_s + (tile & 1)));
                 commit(smem_u32(empty + u % NSLOT));
@@ -627,13 +666,13 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     for (int k = 0; k < 4; ++k)
                         if (k < steps)
                             mma_ta(tm + TM_O, pt + 64 * h + 8 * k, b + k * (2048 >> 4), ID_O,
-                                   (h | k) ? 1u : more);
+                                   k ? 1u : more);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const int part = x >> 2, k = x & 3;
                         if (k < steps)
-                            mma_ta_e4m3(tm + TM_O + 128 * h, pt + 64 * (k >> 1) + 16 * part + 8 * (k & 1),
+                            mma_ta_e4m3(tm + TM_O + 128 * h, pt + 32 * k + 8 * part,
                                         b + k * (4096 >> 4), ID_O, x ? 1u : more);
                     }
                 }
@@ -641,7 +680,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             while (ok && walk.next(p, it)) {
                 if (it.n_kv == 0) continue;
                 const int n = it.b - it.a;
-                ok = mbar_wait(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u, kWaitNs) &&
+                ok = wait_bar(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u) &&
                      score(jt, base + use_k(0));
                 if (n == 1 && ok) commit(smem_u32(q_free));
                 for (int i = 0; i < n && ok; ++i) {
@@ -649,20 +688,19 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         ok = score(jt + i + 1, base + use_k(i + 1));
                         if (i + 2 == n && ok) commit(smem_u32(q_free));
                     }
-                    if (ok && i == 0 && n_item > 0) ok = mbar_wait(o_free, (uint32_t)(n_item - 1) & 1u, kWaitNs);
+                    if (ok && i == 0 && n_item > 0) ok = wait_bar(o_free, (uint32_t)(n_item - 1) & 1u);
                     const int j = jt + i, u0 = base + use_v(i, n);
-                    ok = ok && mbar_wait(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
+                    ok = ok && wait_bar(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u);
                     const int keys = min(KEYS, it.end - (it.a + i) * KEYS);
                     const uint32_t pt = tm + TM_S + 128 * (j & 1);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         ok = ok && full_wait(u0 + h);
                         if (!ok) break;
                         fence_after_sync();
-                        if (keys == KEYS)
-                            weigh(pt, u0 + h, h, 4, i ? 1u : 0u);
-                        else  // bf16: a slot holds 64 of the keys
-                            weigh(pt, u0 + h, h, ((E4M3 ? keys : keys - 64 * h) + STEP - 1) / STEP, i ? 1u : 0u);
+                        // bf16: a slot holds 64 of the keys
+                        weigh(pt, u0 + h, h, ((E4M3 ? keys : keys - 64 * h) + STEP - 1) / STEP,
+                              i || (!E4M3 && h) ? 1u : 0u);
                     }
                     if (!ok) break;
                     commit(smem_u32(bar_o + (j & 1)));
@@ -676,9 +714,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (!ok) report(kTimeout);
         }
         __syncwarp();
-    } else if (E4M3 && warp >= W_AUX) {
+    } else if (E4M3 && warp >= L::W_AUX) {
         // -------------------------------------- Q in two parts, and the scales
-        const int t = tid - 32 * W_AUX;
+        const int t = tid - 32 * L::W_AUX;
         constexpr int NT = 32 * AUX_WARPS;
         float *scales = reinterpret_cast<float *>(sm + L::S_SCALE);
         const float *raw = reinterpret_cast<const float *>(sm + L::S_RAW);
@@ -687,7 +725,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         int jt = 0, n_item = 0;
         while (ok && walk.next(p, it)) {
             if (it.n_kv == 0) continue;
-            ok = __all_sync(kFullMask, mbar_wait(q_full, (uint32_t)n_item & 1u, kWaitNs));
+            ok = __all_sync(kFullMask, wait_bar(q_full, (uint32_t)n_item & 1u));
             if (!ok) break;
             // Row r: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (r % 8).
             for (int r = t; r < it.n_tok * p.n_rep; r += NT) {
@@ -735,9 +773,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_split);
             for (int j = it.a; j < it.b; ++j, ++jt) {
-                ok = mbar_wait(raw_full + jt % NRAW, (uint32_t)(jt / NRAW) & 1u, kWaitNs);
+                ok = wait_bar(raw_full + jt % NRAW, (uint32_t)(jt / NRAW) & 1u);
                 // The stage was read by the softmax two tiles back.
-                if (jt >= 2) ok = ok && mbar_wait(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs);
+                if (jt >= 2) ok = ok && wait_bar(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs);
                 ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 float *st = scales + (jt & 1) * 3 * KEYS;
@@ -759,11 +797,11 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             ++n_item;
         }
         if (!ok && lane == 0) report(kTimeout);
-    } else if (warp < SOFTMAX_WARPS) {
+    } else if (warp < L::SOFTMAX) {
         // -------------------------------------------------------- softmax
-        // Warps w and w + 4 share rows 32 (w % 4) ..; each takes 64 of a tile's keys and
-        // 128 of O's columns.  They agree on a row's maximum through red[], and to
-        // stop, at the same barrier.
+        // The warps w, w + 4, .. share rows 32 (w % 4) ..; each takes KPT of a tile's keys
+        // and COLS of O's columns.  They agree on a row's maximum through red[], and
+        // to stop, at the same barrier.
         //
         // The reference maximum only moves when a tile's maximum passes it by
         // more than kLazy (log2): then O and the sum are rescaled, which needs
@@ -773,15 +811,24 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         constexpr float kLazy = E4M3 ? 2.f : 8.f;
         constexpr float kUp = E4M3 ? 6.f : 0.f;
         constexpr float kShift = E4M3 ? 8.f : 0.f;  // split4 takes weights times 2^-8
-        const int half = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+        constexpr int KPT = KEYS / PARTS, COLS = D / PARTS, NG = 32 * PARTS;
+        const int part = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
         const int tok = r / p.n_rep, h = r - tok * p.n_rep;
         const float *scales = reinterpret_cast<const float *>(sm + L::S_SCALE);
         const float *rowk = reinterpret_cast<const float *>(sm + L::S_ROWK);
+        // The four rows of this lane's group, for stores of 64 bytes a row.
+        const int lane4 = lane & 3;
+        int tok4[4], head4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tok4[k] = (r - lane4 + k) / p.n_rep;
+            head4[k] = r - lane4 + k - tok4[k] * p.n_rep;
+        }
         bool dead = false, fault = false;
         int jt = 0, base = 0, n_item = 0;
         auto wait_o = [&](int tile, uint64_t lim) {
-            return mbar_wait(bar_o + (tile & 1), (uint32_t)(tile >> 1) & 1u, lim);
+            return wait_bar(bar_o + (tile & 1), (uint32_t)(tile >> 1) & 1u, lim);
         };
         while (!dead && walk.next(p, it)) {
             const bool mine = tok < it.n_tok;  // this row exists
@@ -791,12 +838,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (it.n_kv == 0) {
                 // Lengths that cannot be used: zeros.
                 if (mine) {
-                    for (int d = 128 * half; d < 128 * half + 128; d += 4) {
+                    for (int d = COLS * part; d < COLS * part + COLS; d += 4) {
                         using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
                         Elem<T>::store4(static_cast<T *>(p.a.out) + grow * p.a.out_stride + gh * D + d,
                                         make_float4(0.f, 0.f, 0.f, 0.f));
                     }
-                    if (half == 0 && p.a.lse) p.a.lse[grow * p.a.lse_stride + gh] = -INFINITY;
+                    if (part == 0 && p.a.lse) p.a.lse[grow * p.a.lse_stride + gh] = -INFINITY;
                 }
                 continue;
             }
@@ -805,21 +852,28 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             float row_factor = 1.f;
             for (int i = 0; i < n; ++i) {
                 const int j = jt + i, k0 = (it.a + i) * KEYS;
-                bool ok = mbar_wait(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
-                if (E4M3) ok = ok && mbar_wait(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitNs);
+                bool ok = wait_bar(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u);
+                if (E4M3) ok = ok && wait_bar(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u);
                 ok = __all_sync(kFullMask, ok);
-                float s[64];
-                float top = -INFINITY;
-                if (some && ok) {
-                    fence_after_sync();
-                    tmem_ld64(tm + lane_off + TM_S + 128 * (j & 1) + 64 * half, s);
+                // In two passes over the thread's keys, which read S twice and scale it twice:
+                // half the code of holding all of it, and the instruction cache is what the
+                // softmax waits for otherwise.
+                constexpr int CH = KPT / 2;
+                const uint32_t st = tm + lane_off + TM_S + 128 * (j & 1) + KPT * part;
+                const float *sck = scales + (j & 1) * 3 * KEYS + KPT * part;
+                // Keys this row attends, of this thread's (a row that does not exist: all
+                // of them, whatever they are).
+                const int lim = mine ? it.pos0 + tok + 1 - k0 - KPT * part : KPT;
+                const bool masked = __any_sync(kFullMask, lim < KPT);
+                auto load = [&](int c, float (&s)[CH]) {
+                    if constexpr (CH == 32) tmem_ld32(st + CH * c, s);
+                    else tmem_ld16(st + CH * c, s);
                     if constexpr (E4M3) {
-                        if (i == 0) row_factor = rowk[(n_item & 1) * ROWS + r];
-                        const float4 *sk = reinterpret_cast<const float4 *>(scales + (j & 1) * 3 * KEYS + 64 * half);
+                        const float4 *sk = reinterpret_cast<const float4 *>(sck + CH * c);
                         const float4 *lv = sk + KEYS / 4;
                         const float2 rf = make_float2(row_factor, row_factor);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
+                        for (int x = 0; x < CH / 4; ++x) {
                             const float4 a = sk[x], b = lv[x];
                             const float2 u = fma2(mul2(make_float2(s[4 * x], s[4 * x + 1]), rf),
                                                   make_float2(a.x, a.y), make_float2(b.x, b.y));
@@ -831,88 +885,103 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                             s[4 * x + 3] = v.y;
                         }
                     }
-                    // Keys this row attends, of this thread's 64 (a row that does not exist:
-                    // all of them, whatever they are).
-                    const int lim = mine ? it.pos0 + tok + 1 - k0 - 64 * half : 64;
-                    if (__any_sync(kFullMask, lim < 64)) {
+                    if (masked) {
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (x >= lim) s[x] = -INFINITY;
+                        for (int x = 0; x < CH; ++x)
+                            if (x + CH * c >= lim) s[x] = -INFINITY;
                     }
-                    float t4[4] = {s[0], s[1], s[2], s[3]};
+                };
+                float top = -INFINITY;
+                if (some && ok) {
+                    fence_after_sync();
+                    if (E4M3 && i == 0) row_factor = rowk[(n_item & 1) * ROWS + r];
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        float s[CH];
+                        load(c, s);
+                        float t4[4] = {top, s[1], s[2], s[3]};
+                        t4[0] = fmaxf(t4[0], s[0]);
 #pragma unroll
-                    for (int x = 4; x < 64; x += 4) {
-                        t4[0] = fmaxf(t4[0], s[x]);
-                        t4[1] = fmaxf(t4[1], s[x + 1]);
-                        t4[2] = fmaxf(t4[2], s[x + 2]);
-                        t4[3] = fmaxf(t4[3], s[x + 3]);
+                        for (int x = 4; x < CH; x += 4) {
+                            t4[0] = fmaxf(t4[0], s[x]);
+                            t4[1] = fmaxf(t4[1], s[x + 1]);
+                            t4[2] = fmaxf(t4[2], s[x + 2]);
+                            t4[3] = fmaxf(t4[3], s[x + 3]);
+                        }
+                        top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     }
-                    top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     if (!E4M3) top *= p.scale_log2;
-                    red[((j & 1) * 2 + half) * ROWS + r] = top;
+                    red[((j & 1) * PARTS + part) * ROWS + r] = top;
                 }
-                dead = group_sync_or(1 + quad, 64, !ok || fault);
+                dead = group_sync_or(1 + quad, NG, !ok || fault);
                 if (dead) break;
                 if (some) {
-                    top = fmaxf(top, red[((j & 1) * 2 + (half ^ 1)) * ROWS + r]);
+#pragma unroll
+                    for (int x = 1; x < PARTS; ++x)
+                        top = fmaxf(top, red[((j & 1) * PARTS + (part + x) % PARTS) * ROWS + r]);
                     const bool first = m_ref == -INFINITY;
-                    const bool moves = !first && top > m_ref + kLazy;
+                    const bool moves = mine && !first && top > m_ref + kLazy;
                     const float alpha = moves ? exp2_fast(m_ref - top) : 1.f;
                     if (first || moves) m_ref = top;
                     l *= alpha;
                     const bool rescale = __any_sync(kFullMask, moves) && i > 0;
                     // -inf (nothing attended yet) as 0: every exponent below is -inf then.
                     const float sub = (m_ref == -INFINITY ? 0.f : m_ref) - kUp + kShift;
-                    uint32_t pk[32];
-                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
                     const float2 sub2 = make_float2(-sub, -sub);
-                    if constexpr (!E4M3) {
-                        const float2 cl = make_float2(p.scale_log2, p.scale_log2);
+                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+                    // P goes over the S that this warp has read: bf16, 2 keys a column; codes,
+                    // 4 a column, the hi parts of all its keys and then the lo parts.
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        float s[CH];
+                        load(c, s);
+                        uint32_t pk[CH / 2];
+                        if constexpr (!E4M3) {
+                            const float2 cl = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 2) {
-                            const float2 u = fma2(make_float2(s[2 * x], s[2 * x + 1]), cl, sub2);
-                            const float2 v = fma2(make_float2(s[2 * x + 2], s[2 * x + 3]), cl, sub2);
-                            const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
-                            const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                            l2 = add2(l2, a);
-                            l3 = add2(l3, b);
-                            pk[x] = bf16x2(a.x, a.y);
-                            pk[x + 1] = bf16x2(b.x, b.y);
-                        }
-                    } else {
-                        const float4 *rs = reinterpret_cast<const float4 *>(scales + ((j & 1) * 3 + 2) * KEYS + 64 * half);
+                            for (int x = 0; x < CH / 2; x += 2) {
+                                const float2 u = fma2(make_float2(s[2 * x], s[2 * x + 1]), cl, sub2);
+                                const float2 v = fma2(make_float2(s[2 * x + 2], s[2 * x + 3]), cl, sub2);
+                                const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                                const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                                l2 = add2(l2, a);
+                                l3 = add2(l3, b);
+                                pk[x] = bf16x2(a.x, a.y);
+                                pk[x + 1] = bf16x2(b.x, b.y);
+                            }
+                            __syncwarp();
+                            tmem_st16(st + CH / 2 * c, pk);
+                        } else {
+                            const float4 *rs = reinterpret_cast<const float4 *>(sck + 2 * KEYS + CH * c);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float4 f = rs[x];
-                            const float2 u = add2(make_float2(s[4 * x], s[4 * x + 1]), sub2);
-                            const float2 v = add2(make_float2(s[4 * x + 2], s[4 * x + 3]), sub2);
-                            const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
-                            const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
-                            l2 = fma2(a, make_float2(f.x, f.y), l2);
-                            l3 = fma2(b, make_float2(f.z, f.w), l3);
-                            split4(a.x, a.y, b.x, b.y, pk[x], pk[16 + x]);
+                            for (int x = 0; x < CH / 4; ++x) {
+                                const float4 f = rs[x];
+                                const float2 u = add2(make_float2(s[4 * x], s[4 * x + 1]), sub2);
+                                const float2 v = add2(make_float2(s[4 * x + 2], s[4 * x + 3]), sub2);
+                                const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+                                const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
+                                l2 = fma2(a, make_float2(f.x, f.y), l2);
+                                l3 = fma2(b, make_float2(f.z, f.w), l3);
+                                split4(a.x, a.y, b.x, b.y, pk[x], pk[CH / 4 + x]);
+                            }
+                            __syncwarp();
+                            tmem_st4(st + CH / 4 * c, pk[0], pk[1], pk[2], pk[3]);
+                            tmem_st4(st + KPT / 4 + CH / 4 * c, pk[4], pk[5], pk[6], pk[7]);
                         }
                     }
                     l += (l2.x + l2.y) + (l3.x + l3.y);
-                    // Over S: both warps of the rows have read it (the barrier above).
-                    {
-                        float pf[32];
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) pf[x] = __uint_as_float(pk[x]);
-                        __syncwarp();
-                        tmem_st32(tm + lane_off + TM_S + 128 * (j & 1) + 64 * half, pf);
-                    }
+                    tmem_st_wait();
                     if (rescale) {
                         fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs));
                         if (!fault) {
                             fence_after_sync();
 #pragma unroll 1
-                            for (int x = 0; x < 128; x += 32) {
+                            for (int x = 0; x < COLS; x += 32) {
                                 float o[32];
-                                tmem_ld32(tm + lane_off + TM_O + 128 * half + x, o);
+                                tmem_ld32(tm + lane_off + TM_O + COLS * part + x, o);
 #pragma unroll
                                 for (int y = 0; y < 32; ++y) o[y] *= alpha;
-                                tmem_st32(tm + lane_off + TM_O + 128 * half + x, o);
+                                tmem_st32(tm + lane_off + TM_O + COLS * part + x, o);
                             }
                         }
                     }
@@ -931,7 +1000,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     if (!fault) {
                         // 32 16-byte chunks a key: bf16, 4 boxes of 8; codes, 2 slots of 8.
                         constexpr int CH = E4M3 ? 16 : 32;
-                        for (int x = tid; x < (up - keys) * CH; x += 32 * SOFTMAX_WARPS) {
+                        for (int x = tid; x < (up - keys) * CH; x += 32 * L::SOFTMAX) {
                             const int key = keys + x / CH, ch = x % CH;
                             const int uu = E4M3 ? u0 + (ch >> 3) : u;
                             const uint32_t at = ring + (uu % NSLOT) * L::SLOT +
@@ -950,67 +1019,89 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             jt += n;
             base += 4 * n;
             ++n_item;
-            // The item's end: the row's sum over both threads, then O.
+            // The item's end: the row's sum over its threads, then O.
             l *= E4M3 ? 256.f : 1.f;  // 2^kShift
-            red[((jt & 1) * 2 + half) * ROWS + r] = l;
+            red[((jt & 1) * PARTS + part) * ROWS + r] = l;
             const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
-            uint4 gate[16];  // the row's gates, fetched while the last product runs
-            if (whole && mine && p.a.gate) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + 128 * half);
+            // Gates of 32 columns of the lane's four rows, fetched a block ahead.
+            uint4 gates[4] = {};
+            auto fetch_gate = [&](int x) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x) gate[x] = __ldg(src + x);
-            }
+                for (int k = 0; k < 4; ++k)
+                    if (whole && p.a.gate && x < COLS && tok4[k] < it.n_tok)
+                        gates[k] = __ldg(reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(p.a.gate) + (it.row0 + tok4[k]) * p.a.gate_stride +
+                            (it.g * p.n_rep + head4[k]) * D + COLS * part + x + 8 * lane4));
+            };
+            fetch_gate(0);
             const bool ok = wait_o(jt - 1, kWaitNs);
-            dead = group_sync_or(1 + quad, 64, !ok || fault);
+            dead = group_sync_or(1 + quad, NG, !ok || fault);
             if (dead) break;
-            l += red[((jt & 1) * 2 + (half ^ 1)) * ROWS + r];
-            group_sync_or(1 + quad, 64, false);  // the next tile writes there
+            l = 0.f;  // in one order in all its threads
+#pragma unroll
+            for (int x = 0; x < PARTS; ++x) l += red[((jt & 1) * PARTS + x) * ROWS + r];
+            group_sync_or(1 + quad, NG, false);  // the next tile writes there
             fence_after_sync();
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (some) {
-#pragma unroll
-                for (int x = 0; x < 128; x += 32) {
+#pragma unroll 1
+                for (int x = 0; x < COLS; x += 32) {
                     float o[32];
                     __syncwarp();
-                    tmem_ld32(tm + lane_off + TM_O + 128 * half + x, o);
-                    const int d0 = 128 * half + x;
-                    if (!mine) continue;
+                    tmem_ld32(tm + lane_off + TM_O + COLS * part + x, o);
+                    const int d0 = COLS * part + x;
                     if (!whole) {
-                        float *po = p.part_o + ((size_t)slot * ROWS + r) * D + d0;
+                        float4 *po = reinterpret_cast<float4 *>(p.part_o) + ((size_t)slot * (D / 4) + d0 / 4) * ROWS + r;
+                        if (mine)
 #pragma unroll
-                        for (int y = 0; y < 32; y += 4)
-                            *reinterpret_cast<float4 *>(po + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+                            for (int y = 0; y < 8; ++y)
+                                po[y * ROWS] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                         continue;
                     }
-                    const int64_t at = grow * p.a.out_stride + gh * D + d0;
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        float v[8];
+                    for (int y = 0; y < 32; ++y) o[y] *= inv;
+                    if (p.a.gate) {
+                        uint4 g[4];
 #pragma unroll
-                        for (int z = 0; z < 8; ++z) v[z] = o[y + z] * inv;
-                        if (p.a.gate) {
-                            const uint4 g8 = gate[(x + y) >> 3];
-                            const uint32_t gw[4] = {g8.x, g8.y, g8.z, g8.w};
+                        for (int k = 0; k < 4; ++k) g[k] = gates[k];
+                        fetch_gate(x + 32);
+                        transpose4(g, lane);
 #pragma unroll
-                            for (int z = 0; z < 8; ++z) {
-                                const float gt = __uint_as_float(z & 1 ? gw[z >> 1] & 0xffff0000u : gw[z >> 1] << 16);
-                                v[z] = __fdividef(v[z], 1.f + __expf(-gt));
-                            }
+                        for (int y = 0; y < 32; ++y) {
+                            const uint4 c8 = g[y >> 3];
+                            const uint32_t w4[4] = {c8.x, c8.y, c8.z, c8.w};
+                            const uint32_t w = w4[(y & 7) >> 1];
+                            const float gt = __uint_as_float(y & 1 ? w & 0xffff0000u : w << 16);
+                            o[y] = __fdividef(o[y], 1.f + exp2_fast(gt * -1.4426950408889634f));
                         }
-                        if constexpr (OUT_BF16) {
-                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at + y) =
-                                make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                                           bf16x2(v[6], v[7]));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at + y);
-                            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
+                    // 16 bytes of four rows a lane become 64 bytes of a row for four lanes.
+                    constexpr int PER = OUT_BF16 ? 8 : 4;  // values in 16 bytes
+#pragma unroll
+                    for (int y = 0; y < 32; y += 4 * PER) {
+                        uint4 q4[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float *v = o + y + PER * k;
+                            if constexpr (OUT_BF16)
+                                q4[k] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                                   bf16x2(v[6], v[7]));
+                            else
+                                q4[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                   __float_as_uint(v[2]), __float_as_uint(v[3]));
+                        }
+                        transpose4(q4, lane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
+                            T *dst = static_cast<T *>(p.a.out) + (it.row0 + tok4[k]) * p.a.out_stride +
+                                     (it.g * p.n_rep + head4[k]) * D + d0 + y + PER * lane4;
+                            if (tok4[k] < it.n_tok) *reinterpret_cast<uint4 *>(dst) = q4[k];
                         }
                     }
                 }
-                if (mine && half == 0) {
+                if (mine && part == 0) {
                     if (!whole) {
                         float *ml = p.part_ml + ((size_t)slot * ROWS + r) * 2;
                         ml[0] = m_ref - kUp;
@@ -1051,8 +1142,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
 
 // --------------------------------------------------------------- combine
 
-// Block b joins a quarter of the rows of the item that CTA b / 4 began and did not end, a
-// row a warp: y = (sum_i 2^{m_i - m} O_i) / (sum_i 2^{m_i - m} l_i) * sigmoid(gate).
+// COMBINE_SPLIT blocks join the parts of the item that CTA blockIdx.x / COMBINE_SPLIT began
+// and did not end: y = (sum_i 2^{m_i - m} O_i) / (sum_i 2^{m_i - m} l_i) * sigmoid(gate).
+// A warp takes 8 rows (lane % 8) by 16 dims (4 a lane) at a time.
 constexpr int COMBINE_SPLIT = 4;
 constexpr int COMBINE_WARPS = 8;
 template <bool OUT_BF16>
@@ -1070,7 +1162,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
     const Desc d = p.desc[cta];
     if (!d.tail) return;
     const int rows = d.n_tok * p.n_rep;
-    // The parts: slot 2 cta + 1, then slot 2 i of the CTAs after it up to the last part.
+    // The parts: slot 2 cta + 1, then slots 2 i of the CTAs after it up to the last part.
+    // (A CTA between them without one had nothing to do: fewer units than CTAs.)
     int last = cta;
     for (int i0 = cta + 1; i0 < n_cta; i0 += 32) {
         const int i = i0 + lane;
@@ -1081,74 +1174,53 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
         }
         last = min(i0 + 31, n_cta - 1);
     }
-    for (int r = share + COMBINE_SPLIT * warp; r < rows; r += COMBINE_SPLIT * COMBINE_WARPS) {
-        const int tok = r / p.n_rep, h = r - tok * p.n_rep;
-        // The maximum and the sum over the parts, a part a lane.
+    const int n_task = ((rows + 7) >> 3) * (D / 16);
+    for (int task = share * COMBINE_WARPS + warp; task < n_task; task += COMBINE_SPLIT * COMBINE_WARPS) {
+        const int r = (task / (D / 16)) * 8 + (lane & 7), c4 = (task % (D / 16)) * 4 + (lane >> 3);
+        const bool mine = r < rows;
+        // A part's maximum and sum of row r; nothing for a row that does not exist, or a
+        // CTA without a part.
+        auto part_ml = [&](int i) {
+            const bool has = mine && (i == cta || p.desc[i].head != 0);
+            return has ? __ldg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)(2 * i + (i == cta)) * ROWS + r)
+                       : make_float2(-INFINITY, 0.f);
+        };
         float m = -INFINITY;
-        for (int i0 = cta; i0 <= last; i0 += 32) {
-            const int i = i0 + lane;
-            const bool has = i == cta || (i <= last && p.desc[min(i, last)].head != 0);
-            if (has) m = fmaxf(m, p.part_ml[((size_t)(2 * i + (i == cta)) * ROWS + r) * 2]);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-        float l = 0.f, o[8] = {};
-        for (int i0 = cta; i0 <= last; i0 += 32) {
-            const int i = i0 + lane;
-            const bool has = i == cta || (i <= last && p.desc[min(i, last)].head != 0);
-            float f = 0.f;
-            if (has) {
-                const float2 ml = *reinterpret_cast<const float2 *>(
-                    p.part_ml + ((size_t)(2 * i + (i == cta)) * ROWS + r) * 2);
-                // A part in which the row attends nothing has m = -inf and adds nothing.
-                f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
-                l = fmaf(f, ml.y, l);
-            }
-            const int n = min(32, last - i0 + 1);
+        for (int i = cta + (lane >> 3); i <= last; i += 4) m = fmaxf(m, part_ml(i).x);
+        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int x = 0; x < n; ++x) {
-                const float fx = __shfl_sync(kFullMask, f, x);
-                if (fx == 0.f) continue;
-                const int ix = i0 + x;
-                const float4 *po = reinterpret_cast<const float4 *>(
-                    p.part_o + ((size_t)(2 * ix + (ix == cta)) * ROWS + r) * D + 8 * lane);
-                const float4 a = po[0], b = po[1];
-                o[0] = fmaf(fx, a.x, o[0]);
-                o[1] = fmaf(fx, a.y, o[1]);
-                o[2] = fmaf(fx, a.z, o[2]);
-                o[3] = fmaf(fx, a.w, o[3]);
-                o[4] = fmaf(fx, b.x, o[4]);
-                o[5] = fmaf(fx, b.y, o[5]);
-                o[6] = fmaf(fx, b.z, o[6]);
-                o[7] = fmaf(fx, b.w, o[7]);
-            }
+        for (int i = cta; i <= last; ++i) {
+            const float2 ml = part_ml(i);
+            // A part in which the row attends nothing has m = -inf and adds nothing.
+            if (ml.x == -INFINITY) continue;
+            const float f = exp2_fast(ml.x - m);
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p.part_o) +
+                                   ((size_t)(2 * i + (i == cta)) * (D / 4) + c4) * ROWS + r);
+            l = fmaf(f, ml.y, l);
+            o.x = fmaf(f, a.x, o.x);
+            o.y = fmaf(f, a.y, o.y);
+            o.z = fmaf(f, a.z, o.z);
+            o.w = fmaf(f, a.w, o.w);
         }
-        l = group_sum<32>(l);
+        if (!mine) continue;
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int tok = r / p.n_rep, gh = d.g * p.n_rep + r - tok * p.n_rep;
         const int64_t grow = d.row0 + tok;
-        const int gh = d.g * p.n_rep + h;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) o[x] *= inv;
+        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (p.a.gate) {
-            const uint4 g8 = __ldg(reinterpret_cast<const uint4 *>(
-                static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + gh * D + 8 * lane));
-            const uint32_t gw[4] = {g8.x, g8.y, g8.z, g8.w};
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float gt = __uint_as_float(x & 1 ? gw[x >> 1] & 0xffff0000u : gw[x >> 1] << 16);
-                o[x] = __fdividef(o[x], 1.f + __expf(-gt));
-            }
+            const float4 g = Elem<__nv_bfloat16>::load4(static_cast<const __nv_bfloat16 *>(p.a.gate) +
+                                                        grow * p.a.gate_stride + gh * D + 4 * c4);
+            o.x = __fdividef(o.x, 1.f + __expf(-g.x));
+            o.y = __fdividef(o.y, 1.f + __expf(-g.y));
+            o.z = __fdividef(o.z, 1.f + __expf(-g.z));
+            o.w = __fdividef(o.w, 1.f + __expf(-g.w));
         }
-        const int64_t at = grow * p.a.out_stride + gh * D + 8 * lane;
-        if constexpr (OUT_BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.a.out) + at) =
-                make_uint4(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]), bf16x2(o[4], o[5]), bf16x2(o[6], o[7]));
-        } else {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.a.out) + at);
-            dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-        }
-        if (lane == 0 && p.a.lse)
+        using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
+        Elem<T>::store4(static_cast<T *>(p.a.out) + grow * p.a.out_stride + gh * D + 4 * c4, o);
+        if (c4 == 0 && p.a.lse)
             p.a.lse[grow * p.a.lse_stride + gh] =
                 l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
