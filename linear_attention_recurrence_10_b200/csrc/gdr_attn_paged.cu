@@ -55,7 +55,7 @@ constexpr int ROWS = 128;  // query rows per item
 constexpr int KEYS = 128;  // keys per tile
 // Cost of starting and finishing an item, in tiles.
 constexpr int ITEM_COST = 2;
-constexpr int AUX_WARPS = 2;  // split Q, prepare scales: code caches only
+constexpr int AUX_WARPS = 2;      // split Q, prepare scales: code caches only
 constexpr int NRAW = 4;       // tiles of key and value scales in flight
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -69,19 +69,22 @@ constexpr int kTimeout = GDR_ERR_TIMEOUT;
 constexpr uint32_t BOX = 16384;
 template <bool E4M3>
 struct Layout {
+    // Threads that share a row, each with KEYS / PARTS keys of a tile.  Codes take four:
+    // their weights cost three times bf16's instructions, and the split of each row over more
+    // warps hides more of the latency than the smaller register share costs.  bf16 at four:
+    // 3300 clocks a tile instead of 2970, the MMA thread's warp having less of its scheduler.
+    static constexpr int PARTS = E4M3 ? 4 : 2;
+    static constexpr int SOFTMAX = 4 * PARTS;  // softmax warps: 0 ..
+    static constexpr int W_LOAD = SOFTMAX, W_MMA = SOFTMAX + 1, W_AUX = SOFTMAX + 2;
     // A tile is two K slots and two V slots.  bf16: K slots are halves of the dims
     // (2 boxes of [128 keys][64 dims]), V slots halves of the keys (4 boxes of
     // [64 keys][64 dims]).  e4m3: both are halves of the dims ([128 keys][128 dims]).
     static constexpr uint32_t SLOT = E4M3 ? BOX : 2 * BOX;
     static constexpr int NSLOT = E4M3 ? 9 : 5;
-    // Threads that share a row, each with KEYS / PARTS keys of a tile.
-    static constexpr int PARTS = E4M3 ? 4 : 2;
-    static constexpr int SOFTMAX = 4 * PARTS;  // softmax warps: 0 ..
-    static constexpr int W_LOAD = SOFTMAX, W_MMA = SOFTMAX + 1, W_AUX = SOFTMAX + 2;
     static constexpr uint32_t S_Q = 0;
     static constexpr uint32_t S_RING = 4 * BOX;
-    static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;         // [2][PARTS][128] floats
-    static constexpr uint32_t S_SCALE = S_RED + 1024 * PARTS;        // [2][3][128] floats
+    static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;         // [4 quads][2][PARTS][32] floats
+    static constexpr uint32_t S_SCALE = S_RED + 1024 * PARTS;  // [2][3][128] floats
     static constexpr uint32_t S_RAW = S_SCALE + (E4M3 ? 3072 : 0);   // [NRAW][2][128] floats
     static constexpr uint32_t S_ROWK = S_RAW + (E4M3 ? NRAW * 1024 : 0);  // [2][128] floats
     static constexpr uint32_t S_BAR = S_ROWK + (E4M3 ? 1024 : 0);
@@ -104,6 +107,7 @@ struct AttnParams {
     gdr_attn_paged_args a;
     int shift;        // log2(page_size)
     int n_rep, tile_tok;
+    uint32_t rep_inv;  // r / n_rep = r * rep_inv >> 16, for r < 128
     int k_rows, v_rows;  // rows of a K and V box
     int n_rows;       // rows of the cache: a row past the end reads as zeros
     float scale_log2;
@@ -171,10 +175,10 @@ struct Seq {
     }
 };
 
-// Where a CTA's stretch [lo, hi) begins: item (s, g, i), whose cost starts at u.
+// A CTA's stretch: `len` units of cost from its beginning; its first item is (s, g, i), whose
+// cost starts at u <= 0.
 struct Plan {
-    int64_t lo, hi, u;
-    int s, g, i;
+    int len, u, s, g, i;
 };
 
 struct Item {
@@ -194,7 +198,7 @@ struct Walk {
     int n_tiles;
     int next_end, next_len;  // of sequence w.s + 1
     __device__ __forceinline__ Walk(const AttnParams &p, const Plan *plan) : w(*plan), n_tiles(0) {
-        if (w.u < w.hi) {
+        if (w.u < w.len) {
             q.load(p, w.s);
             n_tiles = q.tiles(p);
             fetch(p);
@@ -207,7 +211,7 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const AttnParams &p, Item &it) {
         const gdr_kv_pages &c = p.a.pages;
-        while (w.u < w.hi) {
+        while (w.u < w.len) {
             while (w.i >= n_tiles) {
                 w.i = 0;
                 if (n_tiles == 0 || ++w.g == c.H_kv) {
@@ -226,11 +230,9 @@ struct Walk {
             it.pos0 = q.len + first;
             it.end = it.pos0 + it.n_tok;
             it.n_kv = q.keys(p, w.i);
-            const int64_t from = max(w.lo - w.u - ITEM_COST, (int64_t)0);
-            const int64_t to = min(max(w.hi - w.u - ITEM_COST, (int64_t)0), (int64_t)it.n_kv);
-            const bool begins = w.u >= w.lo;
-            it.a = (int)min(from, (int64_t)it.n_kv);
-            it.b = (int)to;
+            const bool begins = w.u >= 0;
+            it.a = min(max(-w.u - ITEM_COST, 0), it.n_kv);
+            it.b = min(max(w.len - w.u - ITEM_COST, 0), it.n_kv);
             w.u += ITEM_COST + it.n_kv;
             ++w.i;
             if (it.a < it.b || (it.n_kv == 0 && begins)) return true;
@@ -259,7 +261,7 @@ __device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Pla
         if (lane >= o) upto += x;
     }
     if (lane == 31) warp_sum[warp] = upto;
-    if (tid == 0) *plan = Plan{0, 0, 0, 0, 0, 0};
+    if (tid == 0) *plan = Plan{0, 0, 0, 0, 0};
     __syncthreads();
     int64_t before = 0, total = 0;
     for (int i = 0; i < n_warps; ++i) {
@@ -287,7 +289,7 @@ __device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Pla
                     if (u + q.cost(p, m) <= lo) a = m;
                     else b = m;
                 }
-                *plan = Plan{lo, hi, u + q.cost(p, a), s, g, a};
+                *plan = Plan{(int)min(hi - lo, (int64_t)0x3fffffff), (int)(u + q.cost(p, a) - lo), s, g, a};
                 break;
             }
             u += all;
@@ -362,6 +364,21 @@ __device__ __forceinline__ void split2(uint32_t h2, uint16_t &hi, uint16_t &lo) 
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h2), "r"(back));
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
 }
+// a, b times inv and the sigmoids of two bf16 gates, 1 / (1 + 2^u) with u = -g log2(e): one
+// reciprocal for both, of the product (u is held below 60, where the sigmoid is
+// 2^-60 of what it multiplies).
+__device__ __forceinline__ void gate2(float &a, float &b, uint32_t gates, float inv) {
+    const float2 u = mul2(make_float2(__uint_as_float(gates << 16), __uint_as_float(gates & 0xffff0000u)),
+                          make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    const float2 d = add2(make_float2(exp2_fast(fminf(u.x, 60.f)), exp2_fast(fminf(u.y, 60.f))),
+                          make_float2(1.f, 1.f));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
+    r *= inv;
+    const float2 y = mul2(make_float2(a, b), mul2(make_float2(d.y, d.x), make_float2(r, r)));
+    a = y.x;
+    b = y.y;
+}
 // Four weights as e4m3 codes in two parts, with integer instructions: the conversions
 // run at 16 lanes a clock for the SM, like the exponentials beside them.  The weights come
 // times 2^-8, below 2: there f16 has e4m3's exponents (2^-14 its smallest normal value,
@@ -396,22 +413,17 @@ __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
                  : "memory");
 }
 
-// Four 16-byte chunks in each of four neighbouring lanes, transposed: chunk k of lane l
-// goes to chunk l of lane k (its own inverse).
-__device__ __forceinline__ void swap_chunk(uint4 &a, uint4 &b, bool upper, int lanes) {
-    uint4 send = upper ? a : b;
-    send.x = __shfl_xor_sync(kFullMask, send.x, lanes);
-    send.y = __shfl_xor_sync(kFullMask, send.y, lanes);
-    send.z = __shfl_xor_sync(kFullMask, send.z, lanes);
-    send.w = __shfl_xor_sync(kFullMask, send.w, lanes);
-    if (upper) a = send;
-    else b = send;
-}
-__device__ __forceinline__ void transpose4(uint4 (&c)[4], int lane) {
-    swap_chunk(c[0], c[1], lane & 1, 1);
-    swap_chunk(c[2], c[3], lane & 1, 1);
-    swap_chunk(c[0], c[2], lane & 2, 2);
-    swap_chunk(c[1], c[3], lane & 2, 2);
+// Two 16-byte chunks in each of two neighbouring lanes, transposed: the even lane ends
+// with the two first chunks, the odd lane with the two second ones (its own inverse).
+__device__ __forceinline__ void transpose2(uint4 (&c)[2], int lane) {
+    const bool odd = lane & 1;
+    uint4 send = odd ? c[0] : c[1];
+    send.x = __shfl_xor_sync(kFullMask, send.x, 1);
+    send.y = __shfl_xor_sync(kFullMask, send.y, 1);
+    send.z = __shfl_xor_sync(kFullMask, send.z, 1);
+    send.w = __shfl_xor_sync(kFullMask, send.w, 1);
+    if (odd) c[0] = send;
+    else c[1] = send;
 }
 
 // Uses of the ring by an item of n tiles, 4 a tile, in the order the MMA thread takes
@@ -439,7 +451,6 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::S_BAR + 288);
     Plan *plan = reinterpret_cast<Plan *>(sm + L::S_BAR + 304);
     int64_t *warp_sum = reinterpret_cast<int64_t *>(sm + L::S_BAR + 352);  // one a warp
-    float *red = reinterpret_cast<float *>(sm + L::S_RED);
     const gdr_kv_pages &c = p.a.pages;
     // (Through a shuffle, so that the compiler knows the warp's number to be uniform.)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
@@ -814,17 +825,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         constexpr int KPT = KEYS / PARTS, COLS = D / PARTS, NG = 32 * PARTS;
         const int part = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
-        const int tok = r / p.n_rep, h = r - tok * p.n_rep;
+        // The quad's own part of the exchange area: the warps of a quad are in step with each
+        // other, not with those of other quads.  At an item's end it holds the sums.
+        float *red = reinterpret_cast<float *>(sm + L::S_RED) + quad * (2 * PARTS * 32) + lane;
+        const int tok = (int)(r * p.rep_inv >> 16), h = r - tok * p.n_rep;
         const float *scales = reinterpret_cast<const float *>(sm + L::S_SCALE);
         const float *rowk = reinterpret_cast<const float *>(sm + L::S_ROWK);
-        // The four rows of this lane's group, for stores of 64 bytes a row.
-        const int lane4 = lane & 3;
-        int tok4[4], head4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            tok4[k] = (r - lane4 + k) / p.n_rep;
-            head4[k] = r - lane4 + k - tok4[k] * p.n_rep;
-        }
         bool dead = false, fault = false;
         int jt = 0, base = 0, n_item = 0;
         auto wait_o = [&](int tile, uint64_t lim) {
@@ -855,25 +861,24 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 bool ok = wait_bar(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u);
                 if (E4M3) ok = ok && wait_bar(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u);
                 ok = __all_sync(kFullMask, ok);
-                // In two passes over the thread's keys, which read S twice and scale it twice:
-                // half the code of holding all of it, and the instruction cache is what the
-                // softmax waits for otherwise.
-                constexpr int CH = KPT / 2;
+                // bf16: in two chunks of the thread's keys, read twice, which is half the code
+                // of holding all of them (the roles share the instruction cache).  Codes: in one
+                // that is held, since their scaling costs more than the code.
+                constexpr int NCH = KPT / 32;
                 const uint32_t st = tm + lane_off + TM_S + 128 * (j & 1) + KPT * part;
                 const float *sck = scales + (j & 1) * 3 * KEYS + KPT * part;
                 // Keys this row attends, of this thread's (a row that does not exist: all
                 // of them, whatever they are).
                 const int lim = mine ? it.pos0 + tok + 1 - k0 - KPT * part : KPT;
                 const bool masked = __any_sync(kFullMask, lim < KPT);
-                auto load = [&](int c, float (&s)[CH]) {
-                    if constexpr (CH == 32) tmem_ld32(st + CH * c, s);
-                    else tmem_ld16(st + CH * c, s);
+                auto load = [&](int c, float (&s)[32]) {
+                    tmem_ld32(st + 32 * c, s);
                     if constexpr (E4M3) {
-                        const float4 *sk = reinterpret_cast<const float4 *>(sck + CH * c);
+                        const float4 *sk = reinterpret_cast<const float4 *>(sck);
                         const float4 *lv = sk + KEYS / 4;
                         const float2 rf = make_float2(row_factor, row_factor);
 #pragma unroll
-                        for (int x = 0; x < CH / 4; ++x) {
+                        for (int x = 0; x < 8; ++x) {
                             const float4 a = sk[x], b = lv[x];
                             const float2 u = fma2(mul2(make_float2(s[4 * x], s[4 * x + 1]), rf),
                                                   make_float2(a.x, a.y), make_float2(b.x, b.y));
@@ -887,22 +892,22 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     }
                     if (masked) {
 #pragma unroll
-                        for (int x = 0; x < CH; ++x)
-                            if (x + CH * c >= lim) s[x] = -INFINITY;
+                        for (int x = 0; x < 32; ++x)
+                            if (x + 32 * c >= lim) s[x] = -INFINITY;
                     }
                 };
                 float top = -INFINITY;
+                float s[32];
                 if (some && ok) {
                     fence_after_sync();
                     if (E4M3 && i == 0) row_factor = rowk[(n_item & 1) * ROWS + r];
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float s[CH];
+                    for (int c = 0; c < NCH; ++c) {
                         load(c, s);
                         float t4[4] = {top, s[1], s[2], s[3]};
                         t4[0] = fmaxf(t4[0], s[0]);
 #pragma unroll
-                        for (int x = 4; x < CH; x += 4) {
+                        for (int x = 4; x < 32; x += 4) {
                             t4[0] = fmaxf(t4[0], s[x]);
                             t4[1] = fmaxf(t4[1], s[x + 1]);
                             t4[2] = fmaxf(t4[2], s[x + 2]);
@@ -911,14 +916,15 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     }
                     if (!E4M3) top *= p.scale_log2;
-                    red[((j & 1) * PARTS + part) * ROWS + r] = top;
+                    red[((j & 1) * PARTS + part) * 32] = top;
                 }
                 dead = group_sync_or(1 + quad, NG, !ok || fault);
                 if (dead) break;
                 if (some) {
+                    top = -INFINITY;
 #pragma unroll
-                    for (int x = 1; x < PARTS; ++x)
-                        top = fmaxf(top, red[((j & 1) * PARTS + (part + x) % PARTS) * ROWS + r]);
+                    for (int x = 0; x < PARTS; ++x)
+                        top = fmaxf(top, red[((j & 1) * PARTS + x) * 32]);
                     const bool first = m_ref == -INFINITY;
                     const bool moves = mine && !first && top > m_ref + kLazy;
                     const float alpha = moves ? exp2_fast(m_ref - top) : 1.f;
@@ -932,14 +938,13 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     // P goes over the S that this warp has read: bf16, 2 keys a column; codes,
                     // 4 a column, the hi parts of all its keys and then the lo parts.
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float s[CH];
-                        load(c, s);
-                        uint32_t pk[CH / 2];
+                    for (int c = 0; c < NCH; ++c) {
+                        if (NCH > 1) load(c, s);
+                        uint32_t pk[16];
                         if constexpr (!E4M3) {
                             const float2 cl = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-                            for (int x = 0; x < CH / 2; x += 2) {
+                            for (int x = 0; x < 16; x += 2) {
                                 const float2 u = fma2(make_float2(s[2 * x], s[2 * x + 1]), cl, sub2);
                                 const float2 v = fma2(make_float2(s[2 * x + 2], s[2 * x + 3]), cl, sub2);
                                 const float2 a = make_float2(exp2_fast(u.x), exp2_fast(u.y));
@@ -949,12 +954,10 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                                 pk[x] = bf16x2(a.x, a.y);
                                 pk[x + 1] = bf16x2(b.x, b.y);
                             }
-                            __syncwarp();
-                            tmem_st16(st + CH / 2 * c, pk);
                         } else {
-                            const float4 *rs = reinterpret_cast<const float4 *>(sck + 2 * KEYS + CH * c);
+                            const float4 *rs = reinterpret_cast<const float4 *>(sck + 2 * KEYS);
 #pragma unroll
-                            for (int x = 0; x < CH / 4; ++x) {
+                            for (int x = 0; x < 8; ++x) {
                                 const float4 f = rs[x];
                                 const float2 u = add2(make_float2(s[4 * x], s[4 * x + 1]), sub2);
                                 const float2 v = add2(make_float2(s[4 * x + 2], s[4 * x + 3]), sub2);
@@ -962,15 +965,13 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                                 const float2 b = make_float2(exp2_fast(v.x), exp2_fast(v.y));
                                 l2 = fma2(a, make_float2(f.x, f.y), l2);
                                 l3 = fma2(b, make_float2(f.z, f.w), l3);
-                                split4(a.x, a.y, b.x, b.y, pk[x], pk[CH / 4 + x]);
+                                split4(a.x, a.y, b.x, b.y, pk[x], pk[8 + x]);
                             }
-                            __syncwarp();
-                            tmem_st4(st + CH / 4 * c, pk[0], pk[1], pk[2], pk[3]);
-                            tmem_st4(st + KPT / 4 + CH / 4 * c, pk[4], pk[5], pk[6], pk[7]);
                         }
+                        __syncwarp();
+                        tmem_st16(st + 16 * c, pk);
                     }
                     l += (l2.x + l2.y) + (l3.x + l3.y);
-                    tmem_st_wait();
                     if (rescale) {
                         fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs));
                         if (!fault) {
@@ -1021,17 +1022,32 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             ++n_item;
             // The item's end: the row's sum over its threads, then O.
             l *= E4M3 ? 256.f : 1.f;  // 2^kShift
-            red[((jt & 1) * PARTS + part) * ROWS + r] = l;
+            group_sync_or(1 + quad, NG, false);  // every maximum has been read
+            red[part * 32] = l;
             const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
-            // Gates of 32 columns of the lane's four rows, fetched a block ahead.
-            uint4 gates[4] = {};
+            // For accesses of 32 bytes a row, 16 a lane: the two rows of this lane's pair.
+            using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
+            constexpr int PER = 16 / sizeof(T);  // values in 16 bytes
+            const int odd = lane & 1;
+            bool has[2];
+            const uint4 *gate_at[2];
+            T *out_at[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int r2 = r - odd + k, t2 = (int)(r2 * p.rep_inv >> 16);
+                const int col = (it.g * p.n_rep + r2 - t2 * p.n_rep) * D + COLS * part;
+                has[k] = t2 < it.n_tok;
+                gate_at[k] = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.gate) +
+                                                             (it.row0 + t2) * p.a.gate_stride + col + 8 * odd);
+                out_at[k] = static_cast<T *>(p.a.out) + (it.row0 + t2) * p.a.out_stride + col + PER * odd;
+            }
+            // Gates of 16 columns of the pair's rows, fetched a block ahead.
+            const bool gated = whole && p.a.gate;
+            uint4 gates[2] = {};
             auto fetch_gate = [&](int x) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (whole && p.a.gate && x < COLS && tok4[k] < it.n_tok)
-                        gates[k] = __ldg(reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(p.a.gate) + (it.row0 + tok4[k]) * p.a.gate_stride +
-                            (it.g * p.n_rep + head4[k]) * D + COLS * part + x + 8 * lane4));
+                for (int k = 0; k < 2; ++k)
+                    if (gated && has[k] && x < COLS) gates[k] = __ldg(gate_at[k] + x / 8);
             };
             fetch_gate(0);
             const bool ok = wait_o(jt - 1, kWaitNs);
@@ -1039,66 +1055,58 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (dead) break;
             l = 0.f;  // in one order in all its threads
 #pragma unroll
-            for (int x = 0; x < PARTS; ++x) l += red[((jt & 1) * PARTS + x) * ROWS + r];
+            for (int x = 0; x < PARTS; ++x) l += red[x * 32];
             group_sync_or(1 + quad, NG, false);  // the next tile writes there
             fence_after_sync();
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (some) {
 #pragma unroll 1
-                for (int x = 0; x < COLS; x += 32) {
-                    float o[32];
+                for (int x = 0; x < COLS; x += 16) {
+                    float o[16];
                     __syncwarp();
-                    tmem_ld32(tm + lane_off + TM_O + COLS * part + x, o);
-                    const int d0 = COLS * part + x;
+                    tmem_ld16(tm + lane_off + TM_O + COLS * part + x, o);
                     if (!whole) {
-                        float4 *po = reinterpret_cast<float4 *>(p.part_o) + ((size_t)slot * (D / 4) + d0 / 4) * ROWS + r;
+                        float4 *po = reinterpret_cast<float4 *>(p.part_o) +
+                                     ((size_t)slot * (D / 4) + (COLS * part + x) / 4) * ROWS + r;
                         if (mine)
 #pragma unroll
-                            for (int y = 0; y < 8; ++y)
+                            for (int y = 0; y < 4; ++y)
                                 po[y * ROWS] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                         continue;
                     }
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) o[y] *= inv;
                     if (p.a.gate) {
-                        uint4 g[4];
+                        uint4 g[2] = {gates[0], gates[1]};
+                        fetch_gate(x + 16);
+                        transpose2(g, lane);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) g[k] = gates[k];
-                        fetch_gate(x + 32);
-                        transpose4(g, lane);
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) {
+                        for (int y = 0; y < 16; y += 2) {
                             const uint4 c8 = g[y >> 3];
                             const uint32_t w4[4] = {c8.x, c8.y, c8.z, c8.w};
-                            const uint32_t w = w4[(y & 7) >> 1];
-                            const float gt = __uint_as_float(y & 1 ? w & 0xffff0000u : w << 16);
-                            o[y] = __fdividef(o[y], 1.f + exp2_fast(gt * -1.4426950408889634f));
+                            gate2(o[y], o[y + 1], w4[(y & 7) >> 1], inv);
                         }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) o[y] *= inv;
                     }
-                    // 16 bytes of four rows a lane become 64 bytes of a row for four lanes.
-                    constexpr int PER = OUT_BF16 ? 8 : 4;  // values in 16 bytes
+                    // 32 bytes of its row in each lane become 16 bytes of both rows of the pair.
 #pragma unroll
-                    for (int y = 0; y < 32; y += 4 * PER) {
-                        uint4 q4[4];
+                    for (int y = 0; y < 16; y += 2 * PER) {
+                        uint4 q2[2];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 2; ++k) {
                             const float *v = o + y + PER * k;
                             if constexpr (OUT_BF16)
-                                q4[k] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                                q2[k] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
                                                    bf16x2(v[6], v[7]));
                             else
-                                q4[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                q2[k] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
                                                    __float_as_uint(v[2]), __float_as_uint(v[3]));
                         }
-                        transpose4(q4, lane);
+                        transpose2(q2, lane);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
-                            T *dst = static_cast<T *>(p.a.out) + (it.row0 + tok4[k]) * p.a.out_stride +
-                                     (it.g * p.n_rep + head4[k]) * D + d0 + y + PER * lane4;
-                            if (tok4[k] < it.n_tok) *reinterpret_cast<uint4 *>(dst) = q4[k];
-                        }
+                        for (int k = 0; k < 2; ++k)
+                            if (has[k]) *reinterpret_cast<uint4 *>(out_at[k] + x + y) = q2[k];
                     }
                 }
                 if (mine && part == 0) {
@@ -1281,6 +1289,7 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
     p.shift = log2_of(c.page_size);
     p.n_rep = a->H_q / c.H_kv;
     p.tile_tok = ROWS / p.n_rep;
+    p.rep_inv = (65536u + p.n_rep - 1) / p.n_rep;
     const bool codes = c.kv_dtype == GDR_E4M3;
     p.k_rows = c.page_size < KEYS ? c.page_size : KEYS;
     const int v_keys = codes ? KEYS : KEYS / 2;  // keys of a V slot
