@@ -1152,8 +1152,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
 
 // COMBINE_SPLIT blocks join the parts of the item that CTA blockIdx.x / COMBINE_SPLIT began
 // and did not end: y = (sum_i 2^{m_i - m} O_i) / (sum_i 2^{m_i - m} l_i) * sigmoid(gate).
-// A warp takes 8 rows (lane % 8) by 16 dims (4 a lane) at a time.
-constexpr int COMBINE_SPLIT = 4;
+// A warp takes 8 rows (lane % 8) by 16 dims (4 a lane) at a time, the parts four at once: it
+// is a chain of loads, so what counts is how few of them wait for another.
+constexpr int COMBINE_SPLIT = 8;
 constexpr int COMBINE_WARPS = 8;
 template <bool OUT_BF16>
 __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const AttnParams p, int n_cta) {
@@ -1167,11 +1168,9 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
         st = __reduce_max_sync(kFullMask, st);
         if (lane == 0) *p.status = st;
     }
+    // The parts: slot 2 cta + 1, then slots 2 i of the CTAs after it up to the one that ends
+    // the item.  None between is without a part: CTAs with nothing to do come last.
     const Desc d = p.desc[cta];
-    if (!d.tail) return;
-    const int rows = d.n_tok * p.n_rep;
-    // The parts: slot 2 cta + 1, then slots 2 i of the CTAs after it up to the last part.
-    // (A CTA between them without one had nothing to do: fewer units than CTAs.)
     int last = cta;
     for (int i0 = cta + 1; i0 < n_cta; i0 += 32) {
         const int i = i0 + lane;
@@ -1180,51 +1179,56 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
             last = i0 + __ffs(ends) - 1;
             break;
         }
-        last = min(i0 + 31, n_cta - 1);
     }
+    if (!d.tail) return;
+    const int rows = d.n_tok * p.n_rep;
     const int n_task = ((rows + 7) >> 3) * (D / 16);
     for (int task = share * COMBINE_WARPS + warp; task < n_task; task += COMBINE_SPLIT * COMBINE_WARPS) {
         const int r = (task / (D / 16)) * 8 + (lane & 7), c4 = (task % (D / 16)) * 4 + (lane >> 3);
-        const bool mine = r < rows;
-        // A part's maximum and sum of row r; nothing for a row that does not exist, or a
-        // CTA without a part.
-        auto part_ml = [&](int i) {
-            const bool has = mine && (i == cta || p.desc[i].head != 0);
-            return has ? __ldg(reinterpret_cast<const float2 *>(p.part_ml) + (size_t)(2 * i + (i == cta)) * ROWS + r)
-                       : make_float2(-INFINITY, 0.f);
-        };
-        float m = -INFINITY;
-        for (int i = cta + (lane >> 3); i <= last; i += 4) m = fmaxf(m, part_ml(i).x);
-        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = cta; i <= last; ++i) {
-            const float2 ml = part_ml(i);
-            // A part in which the row attends nothing has m = -inf and adds nothing.
-            if (ml.x == -INFINITY) continue;
-            const float f = exp2_fast(ml.x - m);
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p.part_o) +
-                                   ((size_t)(2 * i + (i == cta)) * (D / 4) + c4) * ROWS + r);
-            l = fmaf(f, ml.y, l);
-            o.x = fmaf(f, a.x, o.x);
-            o.y = fmaf(f, a.y, o.y);
-            o.z = fmaf(f, a.z, o.z);
-            o.w = fmaf(f, a.w, o.w);
-        }
-        if (!mine) continue;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (r >= rows) continue;
         const int tok = r / p.n_rep, gh = d.g * p.n_rep + r - tok * p.n_rep;
         const int64_t grow = d.row0 + tok;
+        float4 gate = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.a.gate)
+            gate = Elem<__nv_bfloat16>::load4(static_cast<const __nv_bfloat16 *>(p.a.gate) +
+                                              grow * p.a.gate_stride + gh * D + 4 * c4);
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = cta; i0 <= last; i0 += 4) {
+            float2 ml[4];
+            float4 a[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = min(i0 + k, last);
+                const size_t slot = 2 * i + (i == cta);
+                ml[k] = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + slot * ROWS + r);
+                a[k] = __ldg(reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + c4) * ROWS + r);
+                if (i0 + k > last) ml[k].x = -INFINITY;
+            }
+            const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+            if (top == -INFINITY) continue;
+            const float keep = exp2_fast(m - top);
+            m = top;
+            l *= keep;
+            o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // A part in which the row attends nothing has m = -inf and adds nothing.
+                const float f = exp2_fast(ml[k].x - top);
+                l = fmaf(f, ml[k].y, l);
+                o.x = fmaf(f, a[k].x, o.x);
+                o.y = fmaf(f, a[k].y, o.y);
+                o.z = fmaf(f, a[k].z, o.z);
+                o.w = fmaf(f, a[k].w, o.w);
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
         o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (p.a.gate) {
-            const float4 g = Elem<__nv_bfloat16>::load4(static_cast<const __nv_bfloat16 *>(p.a.gate) +
-                                                        grow * p.a.gate_stride + gh * D + 4 * c4);
-            o.x = __fdividef(o.x, 1.f + __expf(-g.x));
-            o.y = __fdividef(o.y, 1.f + __expf(-g.y));
-            o.z = __fdividef(o.z, 1.f + __expf(-g.z));
-            o.w = __fdividef(o.w, 1.f + __expf(-g.w));
+            o.x = __fdividef(o.x, 1.f + __expf(-gate.x));
+            o.y = __fdividef(o.y, 1.f + __expf(-gate.y));
+            o.z = __fdividef(o.z, 1.f + __expf(-gate.z));
+            o.w = __fdividef(o.w, 1.f + __expf(-gate.w));
         }
         using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
         Elem<T>::store4(static_cast<T *>(p.a.out) + grow * p.a.out_stride + gh * D + 4 * c4, o);
