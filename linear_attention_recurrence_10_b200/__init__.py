@@ -19,6 +19,7 @@ kernels.  PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -391,75 +392,107 @@ def attn_decode_step(q, gate, k, v, k_cache, v_cache, cache_len, out, *, kv_boun
     return out
 
 
+# The paged cache's calls run once per layer and generated token, where the marshalling is
+# most of the time: the C structs are packed by struct (native layout) instead of field by
+# field, and each tensor is asked as little as its checks need.
+_KV_PAGES = "8i q 6P"
+_PACK_APPEND = struct.Struct("@" + _KV_PAGES + " q 2i f i 4q 6P")
+_PACK_GATHER = struct.Struct("@" + _KV_PAGES + " q 2i 2q 4P")
+_PACK_ATTN = struct.Struct("@" + _KV_PAGES + " q 2i f i 4q 5P")
+
+
 def _distinct_rows(t, what):
-    """_row_stride of a tensor whose rows must not be one row expanded (a stride of 0
-    stands for packed rows in the C ABI)."""
+    """Row stride in the C ABI's terms: 0 for packed rows; rows must not be one row expanded."""
+    if t.is_contiguous():
+        return 0
     s = _row_stride(t, what)
     if s == 0 and t.shape[0] > 1:
         raise ValueError(f"{what}: rows are expanded, make it contiguous")
     return s
 
 
+def _ptr0(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale):
-    """The paged cache as the library's struct (gdr_kv_pages)."""
-    if k_pages.dtype == torch.bfloat16:
+    """The paged cache as gdr_kv_pages: (its fields in order, H_kv, d, n_seq)."""
+    dtype, shape = k_pages.dtype, k_pages.shape
+    if dtype is torch.bfloat16:
         code = GDR_BF16
-    elif k_pages.dtype == torch.float8_e4m3fn:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale are given with float8_e4m3fn pages only")
+    elif dtype is torch.float8_e4m3fn:
         code = GDR_E4M3
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is None:
+                raise ValueError(f"float8_e4m3fn pages need {name}")
+            if t.dtype is not torch.float32 or t.shape != shape[:3] or not t.is_contiguous():
+                raise ValueError(f"{name} must be a packed fp32 [n_pages, H_kv, page_size] tensor")
     else:
-        raise TypeError(f"k_pages: dtype {k_pages.dtype} is not bf16 or float8_e4m3fn")
-    shape = k_pages.shape
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dtype != k_pages.dtype:
-            raise TypeError("k_pages and v_pages must have one dtype")
-        if t.dim() != 4 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a packed [n_pages, H_kv, page_size, d] tensor")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if (t is None) != (code == GDR_BF16):
-            raise ValueError(f"{name} is given with float8_e4m3fn pages, and only then")
-        if t is not None and (t.dtype != torch.float32 or t.shape != shape[:3]
-                              or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a packed fp32 [n_pages, H_kv, page_size] tensor")
-    if page_table.dtype != torch.int32 or cu_seqlens.dtype != torch.int32:
+        raise TypeError(f"k_pages: dtype {dtype} is not bf16 or float8_e4m3fn")
+    if v_pages.dtype is not dtype:
+        raise TypeError("k_pages and v_pages must have one dtype")
+    if len(shape) != 4 or v_pages.shape != shape or not k_pages.is_contiguous() \
+            or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be packed [n_pages, H_kv, page_size, d] tensors")
+    if page_table.dtype is not torch.int32 or cu_seqlens.dtype is not torch.int32:
         raise TypeError("page_table and cu_seqlens must be int32")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [n_seq, table_width] with packed rows")
-    n_seq = page_table.shape[0]
-    if n_seq > 1 and page_table.stride(0) < page_table.shape[1]:
-        raise ValueError("page_table's rows must not overlap (an expanded table: make it contiguous)")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != n_seq + 1 or not cu_seqlens.is_contiguous():
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_seq, table_width]")
+    n_seq, width = page_table.shape
+    table_stride = 0
+    if not page_table.is_contiguous():
+        if width > 1 and page_table.stride(1) != 1:
+            raise ValueError("page_table must have packed rows")
+        table_stride = page_table.stride(0) if n_seq > 1 else 0
+        if n_seq > 1 and table_stride < width:
+            raise ValueError("page_table's rows must not overlap (an expanded table: make it "
+                             "contiguous)")
+    if cu_seqlens.shape != (n_seq + 1,) or not cu_seqlens.is_contiguous():
         raise ValueError("cu_seqlens must hold n_seq + 1 entries")
-    return _abi.KvPages(
-        n_seq=n_seq, H_kv=shape[1], d=shape[3], page_size=shape[2], n_pages=shape[0],
-        table_width=page_table.shape[1], kv_dtype=code, reserved=0,
-        table_stride=page_table.stride(0) if n_seq > 1 else 0,
-        k=k_pages.data_ptr(), v=v_pages.data_ptr(), k_scale=_ptr(k_scale), v_scale=_ptr(v_scale),
-        page_table=page_table.data_ptr(), cu_seqlens=cu_seqlens.data_ptr())
+    fields = (n_seq, shape[1], shape[3], shape[2], shape[0], width, code, 0, table_stride,
+              k_pages.data_ptr(), v_pages.data_ptr(), _ptr0(k_scale), _ptr0(v_scale),
+              page_table.data_ptr(), cu_seqlens.data_ptr())
+    return fields, shape[1], shape[3], n_seq
 
 
-def _rows_bf16(t, name, rows, H, d):
-    if t.dtype != torch.bfloat16:
+def _rows_bf16(t, name, shape):
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bf16")
-    if t.shape != (rows, H, d):
-        raise ValueError(f"{name} must be [{rows}, {H}, {d}]")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
 
 
 def _per_seq(t, name, n_seq):
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.dim() != 1 or t.shape[0] != n_seq or not t.is_contiguous():
+    if t.shape != (n_seq,) or not t.is_contiguous():
         raise ValueError(f"{name} must hold n_seq entries")
 
 
 def _status_word(status):
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+    if status is not None and (status.dtype is not torch.int32 or status.numel() < 1):
         raise TypeError("status must be int32")
 
 
-def _one_device(t0, *rest):
-    for t in rest:
-        if t is not None and t.device != t0.device:
-            raise ValueError(f"all tensors must be on one device: {t0.device} and {t.device}")
+def _queue(f, name, packed, more, stream, *tensors):
+    """Call library function f on one device's stream: all tensors' device, made current."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on one device: {tensors[0].device} and {t.device}")
+    if stream is None:
+        handle = torch.cuda.current_stream(index).cuda_stream if index >= 0 else 0
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            status = f(packed, *more, handle)
+    else:
+        status = f(packed, *more, handle)
+    if status:
+        raise GdrError(status, name)
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, cache_len, *, k_scale=None,
@@ -477,28 +510,29 @@ def kv_append(k, v, k_pages, v_pages, page_table, cu_seqlens, cache_len, *, k_sc
     receives q rotated the same way (it may be q).  ``status``: a device int32,
     written only when a token has no valid page.  Returns q_out.
     """
-    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
-    n, H_kv, d = k.shape[0], pages.H_kv, pages.d
-    _rows_bf16(k, "k", n, H_kv, d)
-    _rows_bf16(v, "v", n, H_kv, d)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out are given together")
-    H_q = 0
+    pages, H_kv, d, n_seq = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
+    n = k.shape[0]
+    kv_shape = (n, H_kv, d)
+    _rows_bf16(k, "k", kv_shape)
+    _rows_bf16(v, "v", kv_shape)
+    H_q = q_stride = q_out_stride = 0
     if q is not None:
+        if q_out is None or q.dim() != 3:
+            raise ValueError("q [n_tok, H_q, d] and q_out are given together")
         H_q = q.shape[1]
-        _rows_bf16(q, "q", n, H_q, d)
-        _rows_bf16(q_out, "q_out", n, H_q, d)
-    _per_seq(cache_len, "cache_len", pages.n_seq)
+        shape = (n, H_q, d)
+        _rows_bf16(q, "q", shape)
+        _rows_bf16(q_out, "q_out", shape)
+        q_stride, q_out_stride = _distinct_rows(q, "q"), _distinct_rows(q_out, "q_out")
+    elif q_out is not None:
+        raise ValueError("q and q_out are given together")
+    _per_seq(cache_len, "cache_len", n_seq)
     _status_word(status)
-    _one_device(k, v, k_pages, v_pages, page_table, cu_seqlens, cache_len, k_scale, v_scale, q,
-                q_out, status)
-    a = _abi.KvAppendArgs(
-        pages=pages, n_tok=n, H_q=H_q, rot_dim=int(rot_dim), rope_theta=float(rope_theta),
-        reserved=0, q_stride=_distinct_rows(q, "q") if H_q else 0,
-        q_out_stride=_distinct_rows(q_out, "q_out") if H_q else 0, k_stride=_distinct_rows(k, "k"),
-        v_stride=_distinct_rows(v, "v"), q=_ptr(q), k=_ptr(k), v=_ptr(v), q_out=_ptr(q_out),
-        cache_len=_ptr(cache_len), status=_ptr(status))
-    _check(_abi.lib().gdr_kv_append(ctypes.byref(a), _stream(stream, k.device)), "gdr_kv_append")
+    a = _PACK_APPEND.pack(*pages, n, H_q, int(rot_dim), rope_theta, 0, q_stride, q_out_stride,
+                          _distinct_rows(k, "k"), _distinct_rows(v, "v"), _ptr0(q), k.data_ptr(),
+                          v.data_ptr(), _ptr0(q_out), cache_len.data_ptr(), _ptr0(status))
+    _queue(_abi.lib().gdr_kv_append, "gdr_kv_append", a, (), stream, k, v, k_pages, v_pages,
+           page_table, cu_seqlens, cache_len, k_scale, v_scale, q, q_out, status)
     return q_out
 
 
@@ -511,58 +545,54 @@ def kv_gather(k_pages, v_pages, page_table, cu_seqlens, k_out, v_out, *, k_scale
     device; None: from token 0).  The cache's tensors are those of kv_append.
     Returns (k_out, v_out).
     """
-    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
+    pages, H_kv, d, n_seq = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
     some = k_out if k_out is not None else v_out
     if some is None:
         raise ValueError("one of k_out and v_out is needed")
+    n = some.shape[0]
+    strides = []
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
+            strides.append(0)
             continue
-        if t.dtype != some.dtype:
+        if t.dtype is not some.dtype:
             raise TypeError("k_out and v_out must have one dtype")
-        if t.shape != (some.shape[0], pages.H_kv, pages.d):
+        if t.shape != (n, H_kv, d):
             raise ValueError(f"{name} must be [n_tok, H_kv, d]")
+        strides.append(_distinct_rows(t, name))
     if first is not None:
-        _per_seq(first, "first", pages.n_seq)
+        _per_seq(first, "first", n_seq)
     _status_word(status)
-    _one_device(some, v_out, k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale, first,
-                status)
-    a = _abi.KvGatherArgs(
-        pages=pages, n_tok=some.shape[0], out_dtype=_dtype_code(some, "k_out"), reserved=0,
-        k_out_stride=_distinct_rows(k_out, "k_out") if k_out is not None else 0,
-        v_out_stride=_distinct_rows(v_out, "v_out") if v_out is not None else 0,
-        k_out=_ptr(k_out), v_out=_ptr(v_out), first=_ptr(first), status=_ptr(status))
-    _check(_abi.lib().gdr_kv_gather(ctypes.byref(a), _stream(stream, some.device)), "gdr_kv_gather")
+    a = _PACK_GATHER.pack(*pages, n, _dtype_code(some, "k_out"), 0, *strides, _ptr0(k_out),
+                          _ptr0(v_out), _ptr0(first), _ptr0(status))
+    _queue(_abi.lib().gdr_kv_gather, "gdr_kv_gather", a, (), stream, some, v_out, k_pages, v_pages,
+           page_table, cu_seqlens, k_scale, v_scale, first, status)
     return k_out, v_out
 
 
 def _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale,
                      gate, lse, scale):
-    pages = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
-    d = pages.d
+    pages, H_kv, d, n_seq = _kv_pages(k_pages, v_pages, page_table, cu_seqlens, k_scale, v_scale)
     if q.dim() != 3:
         raise ValueError("q must be [n_tok, H_q, d]")
-    n, H_q = q.shape[0], q.shape[1]
-    _rows_bf16(q, "q", n, H_q, d)
+    n, H_q, _ = shape = q.shape
+    _rows_bf16(q, "q", (n, H_q, d))
+    gate_stride = lse_stride = 0
     if gate is not None:
-        _rows_bf16(gate, "gate", n, H_q, d)
-    if out.shape != q.shape:
+        _rows_bf16(gate, "gate", shape)
+        gate_stride = _distinct_rows(gate, "gate")
+    if out.shape != shape:
         raise ValueError("out must have q's shape")
     if lse is not None:
         _f32_tensor(lse, "lse")
-        if lse.shape != q.shape[:2]:
+        if lse.shape != (n, H_q):
             raise ValueError("lse must be [n_tok, H_q]")
-    _per_seq(cache_len, "cache_len", pages.n_seq)
-    _one_device(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale, gate,
-                lse)
-    return _abi.AttnPagedArgs(
-        pages=pages, n_tok=n, H_q=H_q, out_dtype=_dtype_code(out, "out"),
-        scale=float(d ** -0.5 if scale is None else scale), reserved=0,
-        q_stride=_distinct_rows(q, "q"),
-        gate_stride=_distinct_rows(gate, "gate") if gate is not None else 0,
-        out_stride=_distinct_rows(out, "out"),
-        lse_stride=_distinct_rows(lse, "lse") if lse is not None else 0,
-        q=_ptr(q), gate=_ptr(gate), cache_len=_ptr(cache_len), out=_ptr(out), lse=_ptr(lse))
+        lse_stride = _distinct_rows(lse, "lse")
+    _per_seq(cache_len, "cache_len", n_seq)
+    return _PACK_ATTN.pack(*pages, n, H_q, _dtype_code(out, "out"), d ** -0.5 if scale is None else scale,
+                           0, _distinct_rows(q, "q"), gate_stride, _distinct_rows(out, "out"),
+                           lse_stride, q.data_ptr(), _ptr0(gate), cache_len.data_ptr(),
+                           out.data_ptr(), _ptr0(lse))
 
 
 def attn_paged_workspace_size(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *,
@@ -570,7 +600,7 @@ def attn_paged_workspace_size(q, k_pages, v_pages, page_table, cu_seqlens, cache
     a = _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale,
                          v_scale, gate, lse, scale)
     n = ctypes.c_size_t(0)
-    _check(_abi.lib().gdr_attn_paged_workspace_size(ctypes.byref(a), ctypes.byref(n)),
+    _check(_abi.lib().gdr_attn_paged_workspace_size(a, ctypes.byref(n)),
            "gdr_attn_paged_workspace_size")
     return int(n.value)
 
@@ -594,13 +624,12 @@ def attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *, k
     L = _abi.lib()
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(L.gdr_attn_paged_workspace_size(ctypes.byref(a), ctypes.byref(n)),
-               "gdr_attn_paged_workspace_size")
+        _check(L.gdr_attn_paged_workspace_size(a, ctypes.byref(n)), "gdr_attn_paged_workspace_size")
         if n.value:
             workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(L.gdr_attn_paged(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream(stream, q.device)),
-           "gdr_attn_paged")
+    _queue(L.gdr_attn_paged, "gdr_attn_paged", a, (_ptr0(workspace), ws_bytes), stream, q, k_pages,
+           v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale, gate, lse, workspace)
     return out
 
 

@@ -176,14 +176,15 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
     h.gdr_attn_decode_workspace_size.restype = ctypes.c_int
     h.gdr_attn_decode_step.argtypes = [ctypes.POINTER(AttnDecodeArgs), _vp, ctypes.c_size_t, _vp]
     h.gdr_attn_decode_step.restype = ctypes.c_int
-    h.gdr_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), _vp]
+    # (Pointers as _vp: the binding packs these structs into bytes.)
+    h.gdr_kv_append.argtypes = [_vp, _vp]
     h.gdr_kv_append.restype = ctypes.c_int
-    h.gdr_kv_gather.argtypes = [ctypes.POINTER(KvGatherArgs), _vp]
+    h.gdr_kv_gather.argtypes = [_vp, _vp]
     h.gdr_kv_gather.restype = ctypes.c_int
-    h.gdr_attn_paged_workspace_size.argtypes = [ctypes.POINTER(AttnPagedArgs),
+    h.gdr_attn_paged_workspace_size.argtypes = [_vp,
                                                 ctypes.POINTER(ctypes.c_size_t)]
     h.gdr_attn_paged_workspace_size.restype = ctypes.c_int
-    h.gdr_attn_paged.argtypes = [ctypes.POINTER(AttnPagedArgs), _vp, ctypes.c_size_t, _vp]
+    h.gdr_attn_paged.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
     h.gdr_attn_paged.restype = ctypes.c_int
     h.gdr_moe_workspace_size.argtypes = [ctypes.POINTER(MoeArgs), ctypes.POINTER(ctypes.c_size_t)]
     h.gdr_moe_workspace_size.restype = ctypes.c_int

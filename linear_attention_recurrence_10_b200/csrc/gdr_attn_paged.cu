@@ -39,6 +39,7 @@
 #include "gdr_tmap.cuh"
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "gdr.h"
@@ -738,46 +739,49 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             if (it.n_kv == 0) continue;
             ok = __all_sync(kFullMask, wait_bar(q_full, (uint32_t)n_item & 1u));
             if (!ok) break;
-            // Row r: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (r % 8).
-            for (int r = t; r < it.n_tok * p.n_rep; r += NT) {
-                const uint32_t row = sq + r * 128;
-                auto chunk = [&](int b, int j) { return row + b * BOX + ((j ^ (r & 7)) << 4); };
+            // Row r: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (r % 8).  Eight lanes
+            // a row, each with 16 values of either half: all of a row is read before any of
+            // it is written over.
+            const int oct = lane & 7, n_rows = it.n_tok * p.n_rep;
+#pragma unroll 1
+            for (int r0 = (t >> 5) * 4; r0 < n_rows; r0 += NT / 8) {
+                const int r = r0 + (lane >> 3);
+                auto chunk = [&](int b, int j) { return sq + r * 128 + b * BOX + ((j ^ (r & 7)) << 4); };
+                uint4 x[4];  // values 16 oct .. of half 0 in x[0], x[1], of half 1 in x[2], x[3]
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int j = 2 * oct + (c & 1);
+                    x[c] = ld_shared16(chunk(2 * (c >> 1) + (j >> 3), j & 7));
+                }
                 uint32_t top = 0;  // largest magnitude, as bf16 bits
 #pragma unroll
-                for (int b = 0; b < 4; ++b)
+                for (int c = 0; c < 4; ++c)
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
+                                                 __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 v = ld_shared16(chunk(b, j));
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                    }
+                for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(kFullMask, top, o));
                 // A power of two that takes the largest value into [128, 256).
                 const int e = min(max((int)max(top >> 16, top & 0xffffu) >> 7, 8), 254);
                 const float up = __uint_as_float((uint32_t)(261 - e) << 23);
-                rowk[(n_item & 1) * ROWS + r] = __uint_as_float((uint32_t)(e - 7) << 23);
+                if (oct == 0) rowk[(n_item & 1) * ROWS + r] = __uint_as_float((uint32_t)(e - 7) << 23);
+                __syncwarp();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint4 x[16];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = ld_shared16(chunk(2 * h + (j >> 3), j & 7));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {  // 16 values
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint4 v = x[2 * j + (w >> 1)];
-                            const uint32_t v0 = w & 1 ? v.z : v.x, v1 = w & 1 ? v.w : v.y;
-                            uint16_t h0, h1, l0, l1;
-                            split2(f16x2(__uint_as_float(v0 << 16) * up,
-                                         __uint_as_float(v0 & 0xffff0000u) * up), h0, l0);
-                            split2(f16x2(__uint_as_float(v1 << 16) * up,
-                                         __uint_as_float(v1 & 0xffff0000u) * up), h1, l1);
-                            hi[w] = h0 | (uint32_t)h1 << 16;
-                            lo[w] = l0 | (uint32_t)l1 << 16;
-                        }
-                        st_shared16(chunk(2 * h, j), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                        st_shared16(chunk(2 * h + 1, j), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    for (int w = 0; w < 4; ++w) {
+                        const uint4 v = x[2 * h + (w >> 1)];
+                        const uint32_t v0 = w & 1 ? v.z : v.x, v1 = w & 1 ? v.w : v.y;
+                        uint16_t h0, h1, l0, l1;
+                        split2(f16x2(__uint_as_float(v0 << 16) * up, __uint_as_float(v0 & 0xffff0000u) * up),
+                               h0, l0);
+                        split2(f16x2(__uint_as_float(v1 << 16) * up, __uint_as_float(v1 & 0xffff0000u) * up),
+                               h1, l1);
+                        hi[w] = h0 | (uint32_t)h1 << 16;
+                        lo[w] = l0 | (uint32_t)l1 << 16;
                     }
+                    st_shared16(chunk(2 * h, oct), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    st_shared16(chunk(2 * h + 1, oct), make_uint4(lo[0], lo[1], lo[2], lo[3]));
                 }
             }
             fence_smem_to_async();
@@ -1245,13 +1249,20 @@ size_t ws_ml(int n_cta) { return WS_DESC + (((size_t)n_cta * sizeof(Desc) + 255)
 size_t ws_o(int n_cta) { return ws_ml(n_cta) + (size_t)2 * n_cta * ROWS * 2 * 4; }
 
 template <bool E4M3, bool OUT_BF16>
-cudaError_t launch_attn(const AttnParams &p, int n_cta, cudaStream_t s) {
+cudaError_t launch_attn(const AttnParams &p, int dev, int n_cta, cudaStream_t s) {
     using L = Layout<E4M3>;
     const auto kern = attn_paged_kernel<E4M3, OUT_BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::S_BYTES);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return e;
+    cudaError_t e = cudaSuccess;
+    // The kernel's shared-memory limit, raised once per device (setting it twice is harmless).
+    static std::atomic<uint64_t> raised{0};
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit) || !bit) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::S_BYTES);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return e;
+        }
+        raised.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1313,8 +1324,8 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
                      encode_bf16_2d(&p.tm_v, c.v, D, p.n_rows, D * 2, 64, p.v_rows));
     if (!maps) return cudaErrorInvalidValue;
     const bool bf16 = a->out_dtype == GDR_BF16;
-    if (codes) return bf16 ? launch_attn<true, true>(p, n_sm, s) : launch_attn<true, false>(p, n_sm, s);
-    return bf16 ? launch_attn<false, true>(p, n_sm, s) : launch_attn<false, false>(p, n_sm, s);
+    if (codes) return bf16 ? launch_attn<true, true>(p, dev, n_sm, s) : launch_attn<true, false>(p, dev, n_sm, s);
+    return bf16 ? launch_attn<false, true>(p, dev, n_sm, s) : launch_attn<false, false>(p, dev, n_sm, s);
 }
 
 }  // namespace gdr

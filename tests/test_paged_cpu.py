@@ -304,3 +304,25 @@ def test_binding_refuses_the_rows(change):
 def test_binding_refuses_an_argument(name, change):
     with pytest.raises((TypeError, ValueError)):
         _calls(_tensors(), **change)[name]()
+
+
+def test_packed_structs_are_the_declared_ones():
+    """The binding packs the argument structs by struct formats: the bytes of each are those of
+    the ctypes mirror of include/gdr.h, field for field."""
+    for fmt, cls in ((gdr._PACK_APPEND, _abi.KvAppendArgs), (gdr._PACK_GATHER, _abi.KvGatherArgs),
+                     (gdr._PACK_ATTN, _abi.AttnPagedArgs)):
+        flat = []
+
+        def fields(c, base=0):
+            for name, t in c._fields_:
+                if issubclass(t, ctypes.Structure):
+                    fields(t, base + getattr(c, name).offset)
+                else:
+                    flat.append((base + getattr(c, name).offset, t))
+
+        fields(cls)
+        assert fmt.size == ctypes.sizeof(cls)
+        values = [i + 1 for i in range(len(flat))]
+        data = fmt.pack(*values)
+        for (offset, t), want in zip(flat, values):
+            assert t.from_buffer_copy(data, offset).value == want, (cls.__name__, offset)
