@@ -476,6 +476,11 @@ def _status_word(status):
         raise TypeError("status must be int32")
 
 
+# The current stream's handle without a Stream object around it, where torch has that call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _queue(f, name, packed, more, stream, *tensors):
     """Call library function f on one device's stream: all tensors' device, made current."""
     index = tensors[0].get_device()
@@ -483,7 +488,7 @@ def _queue(f, name, packed, more, stream, *tensors):
         if t is not None and t.get_device() != index:
             raise ValueError(f"all tensors must be on one device: {tensors[0].device} and {t.device}")
     if stream is None:
-        handle = torch.cuda.current_stream(index).cuda_stream if index >= 0 else 0
+        handle = _raw_stream(index) if index >= 0 else 0
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if index >= 0 and index != torch.cuda.current_device():

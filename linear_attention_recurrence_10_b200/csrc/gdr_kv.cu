@@ -22,8 +22,9 @@ namespace gdr {
 namespace paged {
 
 // Tokens per block: a prompt's blocks take several so that a block's set-up
-// (sequence search, angles) is shared; a few tokens spread over the SMs.
-constexpr int TOKENS = 4;
+// (sequence search, pages, angles) is shared; a few tokens spread over the SMs.
+constexpr int APPEND_TOKENS = 16;
+constexpr int GATHER_TOKENS = 32;
 constexpr int WARPS = 8;
 constexpr float kE4m3Max = 448.f;
 
@@ -54,11 +55,53 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Where the block's packed rows t0 .. t0 + n - 1 belong (n <= 32): their token's position and
+// its row of kv head 0 in the cache, -1 without a valid page, or kNone when no sequence
+// owns them.  `before` (may be null) holds each sequence's position of its first row.  Two
+// searches find the sequences of the first and the last row; between them each thread
+// looks by itself, in most blocks at nothing.
+constexpr int kNone = -2;
+struct Where {
+    int first, last;  // sequences
+    int row[32];
+    int64_t pos[32];
+};
+__device__ __forceinline__ void locate(const gdr_kv_pages &c, const int32_t *before, int shift, int64_t t0,
+                                       int n, Where &w) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < 64) {
+        const int s = find_sequence(c.cu_seqlens, c.n_seq, (int)(tid < 32 ? t0 : t0 + n - 1));
+        if (lane == 0) (tid < 32 ? w.first : w.last) = s;
+    }
+    __syncthreads();
+    if (tid < n) {
+        const int t = (int)t0 + tid;
+        int lo = w.first, hi = w.last;  // the first s in [lo, hi] whose end is past t
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (__ldg(c.cu_seqlens + mid + 1) <= t) lo = mid + 1;
+            else hi = mid;
+        }
+        int row = kNone;
+        int64_t pos = 0;
+        if (lo < c.n_seq) {
+            const int i = t - __ldg(c.cu_seqlens + lo);
+            const int from = before ? __ldg(before + lo) : 0;
+            if (i >= 0) {
+                pos = from < 0 ? -1 : (int64_t)from + i;
+                row = cache_row(c, shift, lo, 0, pos);
+            }
+        }
+        w.row[tid] = row;
+        w.pos[tid] = pos;
+    }
+    __syncthreads();
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParams p) {
-    __shared__ float2 turn[TOKENS][D / 2];
-    __shared__ int tok_seq[TOKENS];
-    __shared__ int64_t tok_pos[TOKENS];
+    __shared__ float2 turn[APPEND_TOKENS][D / 2];
+    __shared__ Where where;
     wait_for_predecessor();
     release_dependents();
     const gdr_kv_append_args &a = p.a;
@@ -66,48 +109,41 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int n = (int)min((int64_t)p.tokens, a.n_tok - t0);
-    if (warp < n) {
-        const int t = (int)(t0 + warp);
-        int s = find_sequence(c.cu_seqlens, c.n_seq, t);
-        int64_t pos = 0;
-        if (s < c.n_seq) {
-            const int i = t - __ldg(c.cu_seqlens + s);
-            const int len = __ldg(a.cache_len + s);
-            pos = (int64_t)len + i;
-            if (i < 0) s = c.n_seq;
-            else if (len < 0) pos = -1;  // no valid page
-        }
-        if (lane == 0) {
-            tok_seq[warp] = s;
-            tok_pos[warp] = pos;
-        }
-    }
-    __syncthreads();
+    // Rows of the block: token by token, its q heads, its k heads, its v heads.
+    const int n_rows = n * p.rows, step = gridDim.y * WARPS;
+    auto fetch = [&](int r) {
+        const int tt = r / p.rows, h = r - tt * p.rows;
+        const int64_t t = t0 + tt;
+        const __nv_bfloat16 *src =
+            h < a.H_q             ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride + h * D
+            : h < a.H_q + c.H_kv ? static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride + (h - a.H_q) * D
+                                 : static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride +
+                                       (h - a.H_q - c.H_kv) * D;
+        // Not through the read-only path: q_out may be q.
+        return *reinterpret_cast<const uint4 *>(src + 8 * lane);
+    };
+    int r = blockIdx.y * WARPS + warp;
+    uint4 next = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) next = fetch(r);
+    locate(c, a.cache_len, p.shift, t0, n, where);
     const int half = a.rot_dim >> 1;
     for (int i = threadIdx.x; i < n * half; i += 32 * WARPS) {
         const int tt = i / half, j = i - tt * half;
-        const double ang = (double)tok_pos[tt] * exp2(-(2.0 * j / a.rot_dim) * p.log2_theta);
+        const double ang = (double)where.pos[tt] * exp2(-(2.0 * j / a.rot_dim) * p.log2_theta);
         double sn, cs;
         sincos(ang, &sn, &cs);
         turn[tt][j] = make_float2((float)cs, (float)sn);
     }
     __syncthreads();
-    // Rows of the block: token by token, its q heads, its k heads, its v heads.
-    const int n_rows = n * p.rows;
-    for (int r = blockIdx.y * WARPS + warp; r < n_rows; r += gridDim.y * WARPS) {
+    for (; r < n_rows; r += step) {
+        const uint4 raw = next;
+        if (r + step < n_rows) next = fetch(r + step);  // a row ahead
         const int tt = r / p.rows, h = r - tt * p.rows;
-        const int s = tok_seq[tt];
-        if (s >= c.n_seq) continue;
+        const int row0 = where.row[tt];
+        if (row0 == kNone) continue;
         const int64_t t = t0 + tt;
         const bool is_q = h < a.H_q, is_v = h >= a.H_q + c.H_kv;
         const int g = is_q ? h : is_v ? h - a.H_q - c.H_kv : h - a.H_q;
-        const __nv_bfloat16 *src =
-            (is_q   ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride
-             : is_v ? static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride
-                    : static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride) +
-            g * D;
-        // Not through the read-only path: q_out may be q.
-        const uint4 raw = *reinterpret_cast<const uint4 *>(src + 8 * lane);
         float x[8];
         unpack8(raw, x);
         if (!is_v && half > 0) {
@@ -131,6 +167,9 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
                     }
                 }
             } else {
+                const __nv_bfloat16 *src = (is_q ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride
+                                                 : static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride) +
+                                           g * D;
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -153,11 +192,11 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
             *reinterpret_cast<uint4 *>(dst + 8 * lane) = pack8(x);
             continue;
         }
-        const int row = cache_row(c, p.shift, s, g, tok_pos[tt]);
-        if (row < 0) {
+        if (row0 < 0) {
             if (lane == 0 && a.status) *a.status = kBadPage;
             continue;
         }
+        const int row = row0 + g * c.page_size;
         void *pages = is_v ? c.v : c.k;
         if constexpr (!E4M3) {
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(pages) + (size_t)row * D;
@@ -195,8 +234,7 @@ struct GatherParams {
 
 template <bool E4M3, typename TOUT>
 __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const GatherParams p) {
-    __shared__ int tok_seq[TOKENS];
-    __shared__ int64_t tok_pos[TOKENS];
+    __shared__ Where where;
     wait_for_predecessor();
     release_dependents();
     const gdr_kv_gather_args &a = p.a;
@@ -204,62 +242,64 @@ __global__ void __launch_bounds__(32 * WARPS) kv_gather_kernel(const GatherParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int n = (int)min((int64_t)p.tokens, a.n_tok - t0);
-    if (warp < n) {
-        const int t = (int)(t0 + warp);
-        int s = find_sequence(c.cu_seqlens, c.n_seq, t);
-        int64_t pos = 0;
-        if (s < c.n_seq) {
-            const int i = t - __ldg(c.cu_seqlens + s);
-            const int first = a.first ? __ldg(a.first + s) : 0;
-            pos = first < 0 ? -1 : (int64_t)first + i;
-            if (i < 0) s = c.n_seq;
-        }
-        if (lane == 0) {
-            tok_seq[warp] = s;
-            tok_pos[warp] = pos;
-        }
-    }
-    __syncthreads();
-    const int per_tok = c.H_kv * p.sides, n_rows = n * per_tok;
-    for (int r = blockIdx.y * WARPS + warp; r < n_rows; r += gridDim.y * WARPS) {
-        const int tt = r / per_tok, h = r - tt * per_tok;
-        const int s = tok_seq[tt];
-        if (s >= c.n_seq) continue;
-        const int g = h % c.H_kv;
-        const bool is_v = !a.k_out || h >= c.H_kv;
-        const int row = cache_row(c, p.shift, s, g, tok_pos[tt]);
-        if (row < 0) {
-            if (lane == 0 && a.status) *a.status = kBadPage;
-            continue;
-        }
-        const void *pages = is_v ? c.v : c.k;
-        float x[8];
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if constexpr (E4M3) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
-                static_cast<const unsigned char *>(pages) + (size_t)row * D + 8 * lane));
-            const float scale = __ldg((is_v ? c.v_scale : c.k_scale) + row);
-            const uint32_t ww[2] = {w.x, w.y};
+    locate(c, a.first, p.shift, t0, n, where);
+    // Rows of the block, AHEAD of them in flight a warp.
+    constexpr int AHEAD = 4;
+    const int per_tok = c.H_kv * p.sides, n_rows = n * per_tok, step = gridDim.y * WARPS;
+    for (int r0 = blockIdx.y * WARPS + warp; r0 < n_rows; r0 += AHEAD * step) {
+        uint4 raw[AHEAD];  // codes: 8 bytes and the scale
+        int64_t at[AHEAD];
+        TOUT *to[AHEAD];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)(ww[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-                const float2 f = __half22float2(__half2(h2));
-                x[2 * i] = f.x * scale;
-                x[2 * i + 1] = f.y * scale;
+        for (int k = 0; k < AHEAD; ++k) {
+            to[k] = nullptr;
+            const int r = r0 + k * step;
+            if (r >= n_rows) continue;
+            const int tt = r / per_tok, h = r - tt * per_tok, g = h >= c.H_kv ? h - c.H_kv : h;
+            const int row0 = where.row[tt];
+            if (row0 < 0) {
+                if (row0 != kNone && lane == 0 && a.status) *a.status = kBadPage;
+                continue;
             }
-        } else {
-            raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) +
-                                                        (size_t)row * D + 8 * lane));
-            unpack8(raw, x);
+            const bool is_v = !a.k_out || h >= c.H_kv;
+            const size_t row = (size_t)row0 + (size_t)g * c.page_size;
+            const void *pages = is_v ? c.v : c.k;
+            if constexpr (E4M3) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
+                    static_cast<const unsigned char *>(pages) + row * D + 8 * lane));
+                raw[k] = make_uint4(w.x, w.y, __float_as_uint(__ldg((is_v ? c.v_scale : c.k_scale) + row)), 0);
+            } else {
+                raw[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * D +
+                                                               8 * lane));
+            }
+            to[k] = static_cast<TOUT *>(is_v ? a.v_out : a.k_out);
+            at[k] = (t0 + tt) * (is_v ? a.v_out_stride : a.k_out_stride) + g * D + 8 * lane;
         }
-        const int64_t at = (t0 + tt) * (is_v ? a.v_out_stride : a.k_out_stride) + g * D + 8 * lane;
-        TOUT *dst = static_cast<TOUT *>(is_v ? a.v_out : a.k_out) + at;
-        if constexpr (sizeof(TOUT) == 2) {
-            *reinterpret_cast<uint4 *>(dst) = E4M3 ? pack8(x) : raw;
-        } else {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (!to[k]) continue;
+            TOUT *dst = to[k] + at[k];
+            float x[8];
+            if constexpr (E4M3) {
+                const float scale = __uint_as_float(raw[k].z);
+                const uint32_t ww[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2(
+                        (__nv_fp8x2_storage_t)(ww[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+                    const float2 f = __half22float2(__half2(h2));
+                    x[2 * i] = f.x * scale;
+                    x[2 * i + 1] = f.y * scale;
+                }
+            } else if constexpr (sizeof(TOUT) == 4) {
+                unpack8(raw[k], x);
+            }
+            if constexpr (sizeof(TOUT) == 2) {
+                *reinterpret_cast<uint4 *>(dst) = E4M3 ? pack8(x) : raw[k];
+            } else {
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
         }
     }
 }
@@ -282,12 +322,12 @@ static cudaError_t launch(void (*kern)(P), const P &p, dim3 grid, cudaStream_t s
     return e;
 }
 
-// Below this many tokens a block takes one token and its rows are spread over
-// several blocks, a warp each; above, a block takes TOKENS tokens.
+// Up to this many tokens a block takes one token and its rows are spread over
+// several blocks, a warp each; above, a block takes as many as it can.
 constexpr int64_t kFewTokens = 592;  // 4 blocks for each of 148 SMs
 
-static dim3 grid_for(int64_t n_tok, int rows, int *tokens) {
-    *tokens = n_tok <= kFewTokens ? 1 : TOKENS;
+static dim3 grid_for(int64_t n_tok, int rows, int most, int *tokens) {
+    *tokens = n_tok <= kFewTokens ? 1 : most;
     const unsigned y = *tokens == 1 ? (unsigned)((rows + WARPS - 1) / WARPS) : 1u;
     return dim3((unsigned)((n_tok + *tokens - 1) / *tokens), y < 65535u ? y : 65535u);
 }
@@ -300,7 +340,7 @@ cudaError_t launch_kv_append(const gdr_kv_append_args *a, cudaStream_t s) {
     p.shift = paged::log2_of(a->pages.page_size);
     p.rows = a->H_q + 2 * a->pages.H_kv;
     p.log2_theta = log2((double)a->rope_theta);
-    const dim3 grid = paged::grid_for(a->n_tok, p.rows, &p.tokens);
+    const dim3 grid = paged::grid_for(a->n_tok, p.rows, paged::APPEND_TOKENS, &p.tokens);
     return a->pages.kv_dtype == GDR_E4M3 ? paged::launch(paged::kv_append_kernel<true>, p, grid, s)
                                          : paged::launch(paged::kv_append_kernel<false>, p, grid, s);
 }
@@ -310,7 +350,7 @@ cudaError_t launch_kv_gather(const gdr_kv_gather_args *a, cudaStream_t s) {
     p.a = *a;
     p.shift = paged::log2_of(a->pages.page_size);
     p.sides = (a->k_out ? 1 : 0) + (a->v_out ? 1 : 0);
-    const dim3 grid = paged::grid_for(a->n_tok, p.sides * a->pages.H_kv, &p.tokens);
+    const dim3 grid = paged::grid_for(a->n_tok, p.sides * a->pages.H_kv, paged::GATHER_TOKENS, &p.tokens);
     const bool codes = a->pages.kv_dtype == GDR_E4M3;
     if (a->out_dtype == GDR_BF16)
         return codes ? paged::launch(paged::kv_gather_kernel<true, __nv_bfloat16>, p, grid, s)
