@@ -8,7 +8,7 @@
 //           and codes e4m3(x / scale)
 //   gather: rows scale * codes (or the bf16 rows) into packed rows
 //
-// Both move every byte once and are bound by memory: a warp takes one row of
+// Both move every byte once: a warp takes one row of
 // 256 values, 8 a lane, so that bf16 rows move in 16-byte and codes in 8-byte
 // accesses.  The angles are taken in double, once per token for all its heads.
 #include <cuda_fp8.h>
@@ -32,7 +32,8 @@ struct AppendParams {
     gdr_kv_append_args a;
     int shift;      // log2(page_size)
     int tokens;     // per block
-    int rows;       // per token: H_q + 2 H_kv
+    int rows;       // rows a token that warps take whole: (H_q +) 2 H_kv
+    int whole_q;    // the q heads are among them (a rot_dim that is not a multiple of 16)
     double log2_theta;
 };
 
@@ -109,16 +110,17 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int n = (int)min((int64_t)p.tokens, a.n_tok - t0);
-    // Rows of the block: token by token, its q heads, its k heads, its v heads.
-    const int n_rows = n * p.rows, step = gridDim.y * WARPS;
+    // Rows of the block that a warp takes whole: token by token, its q heads (unless they go
+    // by pairs of chunks, below), its k heads, its v heads.
+    const int n_rows = n * p.rows, step = gridDim.y * WARPS, q_rows = p.whole_q ? a.H_q : 0;
     auto fetch = [&](int r) {
         const int tt = r / p.rows, h = r - tt * p.rows;
         const int64_t t = t0 + tt;
         const __nv_bfloat16 *src =
-            h < a.H_q             ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride + h * D
-            : h < a.H_q + c.H_kv ? static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride + (h - a.H_q) * D
-                                 : static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride +
-                                       (h - a.H_q - c.H_kv) * D;
+            h < q_rows             ? static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride + h * D
+            : h < q_rows + c.H_kv ? static_cast<const __nv_bfloat16 *>(a.k) + t * a.k_stride + (h - q_rows) * D
+                                  : static_cast<const __nv_bfloat16 *>(a.v) + t * a.v_stride +
+                                        (h - q_rows - c.H_kv) * D;
         // Not through the read-only path: q_out may be q.
         return *reinterpret_cast<const uint4 *>(src + 8 * lane);
     };
@@ -135,6 +137,51 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
         turn[tt][j] = make_float2((float)cs, (float)sn);
     }
     __syncthreads();
+    if (!p.whole_q && a.H_q > 0) {
+        // Queries: a thread takes two chunks of 8 values of a row, a chunk to be turned and
+        // its partner, or two of those that stay (which in place it leaves), so that the
+        // arithmetic of the first kind is done by whole warps.
+        const int pairs = half >> 3, others = D / 16 - pairs;
+        const int n_head = n * a.H_q, at = blockIdx.y * (32 * WARPS) + threadIdx.x, by = gridDim.y * (32 * WARPS);
+        auto q_row = [&](int u, int per, int64_t &from, int64_t &to, int &tt) {
+            const int hh = u / per;
+            tt = hh / a.H_q;
+            const int h = hh - tt * a.H_q;
+            from = (t0 + tt) * a.q_stride + h * D;
+            to = (t0 + tt) * a.q_out_stride + h * D;
+            return u - hh * per;
+        };
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
+        __nv_bfloat16 *q_out = static_cast<__nv_bfloat16 *>(a.q_out);
+        for (int u = at; u < n_head * pairs; u += by) {
+            int64_t from, to;
+            int tt;
+            const int j = 8 * q_row(u, pairs, from, to, tt);
+            if (where.row[tt] == kNone) continue;
+            float x[8], y[8], lo[8], hi[8];
+            unpack8(*reinterpret_cast<const uint4 *>(q + from + j), x);
+            unpack8(*reinterpret_cast<const uint4 *>(q + from + half + j), y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 cs = turn[tt][j + i];
+                lo[i] = x[i] * cs.x - y[i] * cs.y;
+                hi[i] = y[i] * cs.x + x[i] * cs.y;
+            }
+            *reinterpret_cast<uint4 *>(q_out + to + j) = pack8(lo);
+            *reinterpret_cast<uint4 *>(q_out + to + half + j) = pack8(hi);
+        }
+        if (q_out != q)
+            for (int u = at; u < n_head * others; u += by) {
+                int64_t from, to;
+                int tt;
+                const int j = a.rot_dim + 16 * q_row(u, others, from, to, tt);
+                if (where.row[tt] == kNone) continue;
+                const uint4 v0 = *reinterpret_cast<const uint4 *>(q + from + j);
+                const uint4 v1 = *reinterpret_cast<const uint4 *>(q + from + j + 8);
+                *reinterpret_cast<uint4 *>(q_out + to + j) = v0;
+                *reinterpret_cast<uint4 *>(q_out + to + j + 8) = v1;
+            }
+    }
     for (; r < n_rows; r += step) {
         const uint4 raw = next;
         if (r + step < n_rows) next = fetch(r + step);  // a row ahead
@@ -142,8 +189,8 @@ __global__ void __launch_bounds__(32 * WARPS) kv_append_kernel(const AppendParam
         const int row0 = where.row[tt];
         if (row0 == kNone) continue;
         const int64_t t = t0 + tt;
-        const bool is_q = h < a.H_q, is_v = h >= a.H_q + c.H_kv;
-        const int g = is_q ? h : is_v ? h - a.H_q - c.H_kv : h - a.H_q;
+        const bool is_q = h < q_rows, is_v = h >= q_rows + c.H_kv;
+        const int g = is_q ? h : is_v ? h - q_rows - c.H_kv : h - q_rows;
         float x[8];
         unpack8(raw, x);
         if (!is_v && half > 0) {
@@ -338,9 +385,10 @@ cudaError_t launch_kv_append(const gdr_kv_append_args *a, cudaStream_t s) {
     paged::AppendParams p = {};
     p.a = *a;
     p.shift = paged::log2_of(a->pages.page_size);
-    p.rows = a->H_q + 2 * a->pages.H_kv;
+    p.whole_q = ((a->rot_dim >> 1) & 7) != 0;
+    p.rows = (p.whole_q ? a->H_q : 0) + 2 * a->pages.H_kv;
     p.log2_theta = log2((double)a->rope_theta);
-    const dim3 grid = paged::grid_for(a->n_tok, p.rows, paged::APPEND_TOKENS, &p.tokens);
+    const dim3 grid = paged::grid_for(a->n_tok, a->H_q + 2 * a->pages.H_kv, paged::APPEND_TOKENS, &p.tokens);
     return a->pages.kv_dtype == GDR_E4M3 ? paged::launch(paged::kv_append_kernel<true>, p, grid, s)
                                          : paged::launch(paged::kv_append_kernel<false>, p, grid, s);
 }
