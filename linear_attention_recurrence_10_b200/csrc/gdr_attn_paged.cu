@@ -107,7 +107,9 @@ struct AttnParams {
     CUtensorMap tm_q, tm_k, tm_v;
     gdr_attn_paged_args a;
     int shift;        // log2(page_size)
-    int n_rep, tile_tok;
+    int n_rep;
+    int cta_tok, tile_tok;  // tokens of a CTA's 128 rows, of an item (twice that for a pair)
+    int pair;               // CTAs of an item: 1 or 2
     uint32_t rep_inv;  // r / n_rep = r * rep_inv >> 16, for r < 128
     int k_rows, v_rows;  // rows of a K and V box
     int n_rows;       // rows of the cache: a row past the end reads as zeros
@@ -184,9 +186,9 @@ struct Plan {
 
 struct Item {
     int s, g;
-    int row0, n_tok;  // packed rows
+    int row0, n_tok;  // packed rows of this CTA
     int pos0;         // position of the first row's token
-    int end;          // keys attended by the last row
+    int end;          // keys attended by the item's last row (of both CTAs of a pair)
     int n_kv;         // tiles of the whole item; 0: lengths not usable
     int a, b;         // this CTA's tiles
 };
@@ -197,8 +199,10 @@ struct Walk {
     Plan w;
     Seq q;
     int n_tiles;
+    int skip;                // tokens of the item before this CTA's
     int next_end, next_len;  // of sequence w.s + 1
-    __device__ __forceinline__ Walk(const AttnParams &p, const Plan *plan) : w(*plan), n_tiles(0) {
+    __device__ __forceinline__ Walk(const AttnParams &p, const Plan *plan, int rank)
+        : w(*plan), n_tiles(0), skip(rank * p.cta_tok) {
         if (w.u < w.len) {
             q.load(p, w.s);
             n_tiles = q.tiles(p);
@@ -226,10 +230,10 @@ struct Walk {
             const int first = w.i * p.tile_tok;
             it.s = w.s;
             it.g = w.g;
-            it.row0 = q.cu0 + first;
-            it.n_tok = min(p.tile_tok, q.q - first);
-            it.pos0 = q.len + first;
-            it.end = it.pos0 + it.n_tok;
+            it.row0 = q.cu0 + first + skip;
+            it.n_tok = min(p.cta_tok, max(q.q - first - skip, 0));
+            it.pos0 = q.len + first + skip;
+            it.end = q.len + min(first + p.tile_tok, q.q);
             it.n_kv = q.keys(p, w.i);
             const bool begins = w.u >= 0;
             it.a = min(max(-w.u - ITEM_COST, 0), it.n_kv);
@@ -271,9 +275,9 @@ __device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Pla
     }
     upto += before;
     // (blockIdx * total could overflow.)
-    const int64_t n = gridDim.x, each = total / n, more = total - each * n;
-    const int64_t lo = blockIdx.x * each + min((int64_t)blockIdx.x, more);
-    const int64_t hi = lo + each + (blockIdx.x < more ? 1 : 0);
+    const int64_t n = gridDim.x / p.pair, me = blockIdx.x / p.pair, each = total / n, more = total - each * n;
+    const int64_t lo = me * each + min(me, more);
+    const int64_t hi = lo + each + (me < more ? 1 : 0);
     int64_t u = upto - mine;
     if (lo < hi && u <= lo && lo < upto) {
         for (int s = s0; s < s1; ++s) {
@@ -427,16 +431,19 @@ __device__ __forceinline__ void transpose2(uint4 (&c)[2], int lane) {
     else c[1] = send;
 }
 
-// Uses of the ring by an item of n tiles, 4 a tile, in the order the MMA thread takes
-// them: K0, K1, V0, K2, V1, ..., V(n-1).
-__device__ __forceinline__ int use_k(int i) { return i == 0 ? 0 : 4 * i - 2; }
-__device__ __forceinline__ int use_v(int i, int n) { return i < n - 1 ? 4 * i + 4 : 4 * n - 2; }
+// Uses of the ring by an item of n tiles, in the order the MMA thread takes them: K0, K1,
+// V0, K2, V1, ..., V(n-1), each SPT slots.
+template <int SPT>
+__device__ __forceinline__ int use_k(int i) { return i == 0 ? 0 : SPT * (2 * i - 1); }
+template <int SPT>
+__device__ __forceinline__ int use_v(int i, int n) { return SPT * (i < n - 1 ? 2 * i + 2 : 2 * n - 1); }
 
-template <bool E4M3, bool OUT_BF16>
+template <bool E4M3, bool PAIR, bool OUT_BF16>
 __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     attn_paged_kernel(const __grid_constant__ AttnParams p) {
     using L = Layout<E4M3>;
-    constexpr int NSLOT = L::NSLOT, PARTS = L::PARTS;
+    static_assert(!(E4M3 && PAIR), "code caches are not paired");
+    constexpr int NSLOT = L::NSLOT, PARTS = L::PARTS, SPT = PAIR ? 1 : 2;
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::S_BAR);  // [NSLOT] slot landed
     uint64_t *empty = full + NSLOT;    // [NSLOT] slot consumed
@@ -449,6 +456,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     uint64_t *o_free = q_full + 9;     // the item's O has been read (8 warps)
     uint64_t *sc_full = q_full + 10;   // [2] scales of a tile prepared (aux warps)
     uint64_t *raw_full = q_full + 12;  // [NRAW] scales of a tile landed
+    uint64_t *peer_full = q_full + 12;  // [NSLOT] pairs: slot landed in the odd CTA (no codes there)
+    uint64_t *peer_q = peer_full + NSLOT;  // pairs: Q tile landed in the odd CTA
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::S_BAR + 288);
     Plan *plan = reinterpret_cast<Plan *>(sm + L::S_BAR + 304);
     int64_t *warp_sum = reinterpret_cast<int64_t *>(sm + L::S_BAR + 352);  // one a warp
@@ -457,8 +466,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFullMask, tid >> 5, 0);
     const uint32_t sbase = smem_u32(sm);
     const uint32_t ring = sbase + L::S_RING, sq = sbase + L::S_Q;
+    const int rank = PAIR ? (int)cluster_rank() : 0;
 
-    if (warp == 0) tmem_alloc(tmem_slot, TM_COLS);
+    if (warp == 0) {
+        if constexpr (PAIR) tmem_alloc_pair(tmem_slot, TM_COLS);
+        else tmem_alloc(tmem_slot, TM_COLS);
+    }
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) {
             mbar_init(full + i, 1);
@@ -469,12 +482,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + i, 1);
-            mbar_init(bar_p + i, L::SOFTMAX);
+            mbar_init(bar_p + i, (PAIR ? 2 : 1) * L::SOFTMAX);
             mbar_init(bar_o + i, 1);
             mbar_init(sc_full + i, AUX_WARPS);
         }
-        for (int i = 0; i < NRAW; ++i) mbar_init(raw_full + i, 1);
-        mbar_init(o_free, L::SOFTMAX);
+        for (int i = 0; i < (PAIR ? NSLOT + 1 : NRAW); ++i) mbar_init(raw_full + i, 1);  // (peer_full, peer_q)
+        mbar_init(o_free, (PAIR ? 2 : 1) * L::SOFTMAX);
         mbar_fence_init();
     }
     wait_for_predecessor();
@@ -484,6 +497,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     make_plan(p, L::THREADS, warp_sum, plan);
     fence_before_sync();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // the barriers of both CTAs are set up
     fence_after_sync();
     const uint32_t tm = *tmem_slot;
     auto report = [&](int status) { atomicMax(&desc->status, status); };
@@ -494,7 +508,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     const bool usable = (sbase & 1023u) == 0;
     if (!usable && tid == 0) report(GDR_ERR_CUDA);
 
-    Walk walk(p, plan);
+    // Arrivals that the thread which issues the MMAs waits for, in its CTA.
+    auto arrive_mma = [&](uint64_t *bar) {
+        if (PAIR && rank) mbar_arrive_at(bar, 0);
+        else mbar_arrive(bar);
+    };
+    Walk walk(p, plan, rank);
     Item it;
     if (!usable) {
         // nothing runs
@@ -537,18 +556,24 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             };
             auto load_k = [&](int j, int use0, int row) {
                 const int n = min(KEYS, it.end - j * KEYS);
-                const int parts = (n + kr - 1) / kr;
-                constexpr int NCOL = E4M3 ? 1 : 2;
-                for (int h = 0; h < 2; ++h) {
+                // Pairs: this CTA's 64 keys, in boxes of 64 dims as V's below.
+                const int keys = PAIR ? max(0, min(64, n - 64 * rank)) : n;
+                const int parts = (keys + kr - 1) / kr;
+                constexpr int NCOL = E4M3 ? 1 : PAIR ? 4 : 2;
+                constexpr uint32_t COL = PAIR ? BOX / 2 : BOX;
+                for (int h = 0; h < SPT; ++h) {
                     const int use = use0 + h;
                     if (!acquire(use)) return;
                     uint64_t *bar = full + use % NSLOT;
-                    if (lane == 0) bulk_expect(bar, (uint32_t)(parts * NCOL * kr * 128));
+                    if (lane == 0) {
+                        if (!PAIR || parts > 0) bulk_expect(bar, (uint32_t)(parts * NCOL * kr * 128));
+                        else mbar_arrive(bar);
+                    }
                     __syncwarp();
                     const int part = lane / NCOL, col = lane % NCOL;
-                    const int r = __shfl_sync(kFullMask, row, (part * (kr >> 4)) & 7);
+                    const int r = __shfl_sync(kFullMask, row, (part * (kr >> 4) + (PAIR ? 4 * rank : 0)) & 7);
                     if (part < parts)
-                        tma_load_2d(ring + (use % NSLOT) * L::SLOT + col * BOX + part * kr * 128,
+                        tma_load_2d(ring + (use % NSLOT) * L::SLOT + col * COL + part * kr * 128,
                                     &p.tm_k, h * 128 + col * 64, r, bar);
                     n_use = use + 1;
                 }
@@ -572,13 +597,16 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             };
             auto load_v = [&](int j, int use0, int row) {
                 const int n = min(KEYS, it.end - j * KEYS);
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < SPT; ++h) {
                     const int use = use0 + h;
                     if (!acquire(use)) return;
                     uint64_t *bar = full + use % NSLOT;
                     const uint32_t dst = ring + (use % NSLOT) * L::SLOT;
-                    constexpr int NCOL = E4M3 ? 1 : 4;
-                    const int keys = E4M3 ? n : max(0, min(64, n - 64 * h));
+                    // bf16: half of the keys, all dims; pairs and codes: all keys, half of the dims
+                    constexpr bool BY_DIMS = E4M3 || PAIR;
+                    constexpr int NCOL = E4M3 ? 1 : PAIR ? 2 : 4;
+                    constexpr uint32_t COL = PAIR ? BOX : BOX / 2;
+                    const int keys = BY_DIMS ? n : max(0, min(64, n - 64 * h));
                     const int parts = (keys + vr - 1) / vr;
                     if (lane == 0) {
                         if (parts > 0) bulk_expect(bar, (uint32_t)(parts * NCOL * vr * 128));
@@ -586,10 +614,10 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     }
                     __syncwarp();
                     const int part = lane / NCOL, col = lane % NCOL;
-                    const int r = __shfl_sync(kFullMask, row, (part * (vr >> 4) + (E4M3 ? 0 : 4 * h)) & 7);
+                    const int r = __shfl_sync(kFullMask, row, (part * (vr >> 4) + (BY_DIMS ? 0 : 4 * h)) & 7);
                     if (part < parts)
-                        tma_load_2d(dst + col * (BOX / 2) + part * vr * 128, &p.tm_v,
-                                    E4M3 ? h * 128 : col * 64, r, bar);
+                        tma_load_2d(dst + col * COL + part * vr * 128, &p.tm_v,
+                                    (BY_DIMS ? (PAIR ? rank : h) * 128 : 0) + col * 64, r, bar);
                     n_use = use + 1;
                 }
             };
@@ -602,16 +630,16 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             }
             ++n_item;
             if (lane == 0) {
-                bulk_expect(q_full, (uint32_t)(4 * 128 * p.n_rep * p.tile_tok));
+                bulk_expect(q_full, (uint32_t)(4 * 128 * p.n_rep * p.cta_tok));
                 for (int b = 0; b < 4; ++b)
                     tma_load_3d(sq + b * BOX, &p.tm_q, b * 64, it.g * p.n_rep, it.row0, q_full);
             }
             __syncwarp();
-            load_k(it.a, base + use_k(0), row);
+            load_k(it.a, base + use_k<SPT>(0), row);
             for (int i = 0; i < n && ok; ++i) {
                 const int row2 = page_row(it.a + i + 2);
-                if (i + 1 < n) load_k(it.a + i + 1, base + use_k(i + 1), row1);
-                if (ok) load_v(it.a + i, base + use_v(i, n), row);
+                if (i + 1 < n) load_k(it.a + i + 1, base + use_k<SPT>(i + 1), row1);
+                if (ok) load_v(it.a + i, base + use_v<SPT>(i, n), row);
                 row = row1;
                 row1 = row2;
             }
@@ -639,14 +667,39 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         // ------------------------------------------------------ MMA issue
         // One elected thread.  Descriptors are a base per operand plus a constant step:
         // what is left to compute per instruction is one addition.
-        if (elect_one()) {
+        if (PAIR && rank) {
+            // The odd CTA tells the issuing thread what has landed here.
+            if (elect_one()) {
+                bool ok = true;
+                int u = 0, n_item = 0;
+                while (ok && walk.next(p, it)) {
+                    if (it.n_kv == 0) continue;
+                    ok = wait_bar(q_full, (uint32_t)n_item & 1u);
+                    if (ok) mbar_arrive_at(peer_q, 0);
+                    for (const int end = u + 2 * (it.b - it.a); u < end && ok; ++u) {
+                        ok = full_wait(u);
+                        if (ok) mbar_arrive_at(peer_full + u % NSLOT, 0);
+                    }
+                    ++n_item;
+                }
+                if (!ok) report(kTimeout);
+            }
+        } else if (elect_one()) {
             constexpr Kind KIND = E4M3 ? Kind::E4M3 : Kind::BF16;
-            constexpr uint32_t ID_S = instr_desc<KIND>(128, KEYS, false, false);
-            constexpr uint32_t ID_O = instr_desc<KIND>(128, E4M3 ? 128 : 256, false, true);
+            constexpr int M = PAIR ? 256 : 128;
+            constexpr uint32_t ID_S = instr_desc<KIND>(M, KEYS, false, false);
+            constexpr uint32_t ID_O = instr_desc<KIND>(M, E4M3 ? 128 : 256, false, true);
             constexpr int STEP = E4M3 ? 32 : 16;  // keys per instruction of P V
             const uint64_t dq = smem_desc_sw128(sq, 16, 1024);
             const uint64_t dk = smem_desc_sw128(ring, 16, 1024);
-            const uint64_t dv = smem_desc_sw128(ring, E4M3 ? BOX : BOX / 2, 1024);
+            const uint64_t dv = smem_desc_sw128(ring, E4M3 || PAIR ? BOX : BOX / 2, 1024);
+            auto done = [&](uint64_t *bar) {
+                if constexpr (PAIR) commit_pair(smem_u32(bar));
+                else commit(smem_u32(bar));
+            };
+            auto landed = [&](int u) {  // in both CTAs of a pair
+                return full_wait(u) && (!PAIR || wait_bar(peer_full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u));
+            };
             bool ok = true;
             int jt = 0, base = 0, n_item = 0;
             // S of tile `tile`, from the ring's uses u, u + 1.
@@ -654,26 +707,36 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 const uint32_t d = tm + TM_S + 128 * (tile & 1);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    if (!full_wait(u + h)) return false;
+                    const int use = u + (SPT == 2 ? h : 0);
+                    if ((SPT == 2 || h == 0) && !landed(use)) return false;
                     fence_after_sync();
                     const uint64_t a = dq + (uint64_t)h * (2 * BOX >> 4);
-                    const uint64_t b = dk + (uint64_t)((u + h) % NSLOT) * (L::SLOT >> 4);
+                    const uint64_t b = dk + (uint64_t)(use % NSLOT) * (L::SLOT >> 4) + (PAIR ? h * (BOX >> 4) : 0);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        // bf16: box k / 4 of the half; e4m3: the hi, then the lo part
-                        mma<KIND>(d, a + ((k >> 2) * (BOX >> 4) + (k & 3) * 2),
-                                  b + ((E4M3 ? 0 : (k >> 2) * (BOX >> 4)) + (k & 3) * 2), ID_S,
-                                  k ? 1u : (uint32_t)h);
+                    for (int k = 0; k < 8; ++k) {
+                        // bf16: box k / 4 of the half (a pair's boxes have 64 keys); e4m3: the hi,
+                        // then the lo part
+                        constexpr uint32_t KBOX = PAIR ? BOX / 2 : BOX;
+                        const uint64_t ak = a + ((k >> 2) * (BOX >> 4) + (k & 3) * 2);
+                        const uint64_t bk = b + ((E4M3 ? 0 : (k >> 2) * (KBOX >> 4)) + (k & 3) * 2);
+                        if constexpr (PAIR) mma_pair(d, ak, bk, ID_S, k ? 1u : (uint32_t)h);
+                        else mma<KIND>(d, ak, bk, ID_S, k ? 1u : (uint32_t)h);
+                    }
                 }
-                commit(smem_u32(bar_s + (tile & 1)));
-                commit(smem_u32(empty + u % NSLOT));
-                commit(smem_u32(empty + (u + 1) % NSLOT));
+                done(bar_s + (tile & 1));
+                for (int h = 0; h < SPT; ++h) done(empty + (u + h) % NSLOT);
                 return true;
             };
             // O (+)= P V of half h of a tile: `steps` instructions, twice (hi, lo) for codes.
             auto weigh = [&](uint32_t pt, int u, int h, int steps, uint32_t more) {
                 const uint64_t b = dv + (uint64_t)(u % NSLOT) * (L::SLOT >> 4);
-                if constexpr (!E4M3) {
+                if constexpr (PAIR) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < steps)
+                            mma_pair_ta(tm + TM_O, pt + 64 * (k >> 2) + 8 * (k & 3), b + k * (2048 >> 4), ID_O,
+                                        k ? 1u : more);
+                } else if constexpr (!E4M3) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (k < steps)
@@ -693,34 +756,33 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 if (it.n_kv == 0) continue;
                 const int n = it.b - it.a;
                 ok = wait_bar(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u) &&
-                     score(jt, base + use_k(0));
-                if (n == 1 && ok) commit(smem_u32(q_free));
+                     (!PAIR || wait_bar(peer_q, (uint32_t)n_item & 1u)) && score(jt, base + use_k<SPT>(0));
+                if (n == 1 && ok) done(q_free);
                 for (int i = 0; i < n && ok; ++i) {
                     if (i + 1 < n) {
-                        ok = score(jt + i + 1, base + use_k(i + 1));
-                        if (i + 2 == n && ok) commit(smem_u32(q_free));
+                        ok = score(jt + i + 1, base + use_k<SPT>(i + 1));
+                        if (i + 2 == n && ok) done(q_free);
                     }
                     if (ok && i == 0 && n_item > 0) ok = wait_bar(o_free, (uint32_t)(n_item - 1) & 1u);
-                    const int j = jt + i, u0 = base + use_v(i, n);
+                    const int j = jt + i, u0 = base + use_v<SPT>(i, n);
                     ok = ok && wait_bar(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u);
                     const int keys = min(KEYS, it.end - (it.a + i) * KEYS);
                     const uint32_t pt = tm + TM_S + 128 * (j & 1);
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && full_wait(u0 + h);
+                    for (int h = 0; h < SPT; ++h) {
+                        ok = ok && landed(u0 + h);
                         if (!ok) break;
                         fence_after_sync();
                         // bf16: a slot holds 64 of the keys
-                        weigh(pt, u0 + h, h, ((E4M3 ? keys : keys - 64 * h) + STEP - 1) / STEP,
+                        weigh(pt, u0 + h, h, ((E4M3 || PAIR ? keys : keys - 64 * h) + STEP - 1) / STEP,
                               i || (!E4M3 && h) ? 1u : 0u);
                     }
                     if (!ok) break;
-                    commit(smem_u32(bar_o + (j & 1)));
-                    commit(smem_u32(empty + u0 % NSLOT));
-                    commit(smem_u32(empty + (u0 + 1) % NSLOT));
+                    done(bar_o + (j & 1));
+                    for (int h = 0; h < SPT; ++h) done(empty + (u0 + h) % NSLOT);
                 }
                 jt += n;
-                base += 4 * n;
+                base += 2 * SPT * n;
                 ++n_item;
             }
             if (!ok) report(kTimeout);
@@ -997,20 +1059,20 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 constexpr int STEP = E4M3 ? 32 : 16;
                 if (keys < KEYS && (keys & (STEP - 1))) {
                     const int up = (keys + STEP - 1) & ~(STEP - 1);
-                    const int u0 = base + use_v(i, n);
-                    const int u = E4M3 ? u0 : u0 + (keys >> 6);
+                    // 16 bytes each: bf16, 4 boxes of 8 a key; pairs, 2 boxes; codes, 2 slots.
+                    constexpr int CH = E4M3 || PAIR ? 16 : 32;
+                    constexpr uint32_t COL = PAIR ? BOX : BOX / 2;
+                    const int u0 = base + use_v<SPT>(i, n);
+                    const int u = E4M3 || PAIR ? u0 : u0 + (keys >> 6);
                     bool okv = full_wait(u);
                     if (E4M3) okv = okv && full_wait(u0 + 1);
                     fault = fault || !__all_sync(kFullMask, okv);
                     if (!fault) {
-                        // 32 16-byte chunks a key: bf16, 4 boxes of 8; codes, 2 slots of 8.
-                        constexpr int CH = E4M3 ? 16 : 32;
                         for (int x = tid; x < (up - keys) * CH; x += 32 * L::SOFTMAX) {
                             const int key = keys + x / CH, ch = x % CH;
                             const int uu = E4M3 ? u0 + (ch >> 3) : u;
-                            const uint32_t at = ring + (uu % NSLOT) * L::SLOT +
-                                                (E4M3 ? 0 : (ch >> 3) * (BOX / 2)) +
-                                                (E4M3 ? key : key & 63) * 128 + (ch & 7) * 16;
+                            const uint32_t at = ring + (uu % NSLOT) * L::SLOT + (E4M3 ? 0 : (ch >> 3) * COL) +
+                                                (E4M3 || PAIR ? key : key & 63) * 128 + (ch & 7) * 16;
                             st_shared16(at, make_uint4(0, 0, 0, 0));
                         }
                     }
@@ -1018,11 +1080,11 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 }
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_p + (j & 1));
+                if (lane == 0) arrive_mma(bar_p + (j & 1));
             }
             if (dead) break;
             jt += n;
-            base += 4 * n;
+            base += 2 * SPT * n;
             ++n_item;
             // The item's end: the row's sum over its threads, then O.
             l *= E4M3 ? 256.f : 1.f;  // 2^kShift
@@ -1126,7 +1188,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             }
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
+            if (lane == 0) arrive_mma(o_free);
             if (!whole && tid == 0) {
                 if (!begins) {
                     desc->head = ends ? 2 : 1;
@@ -1146,9 +1208,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
 
     fence_before_sync();
     __syncthreads();
+    // Neither CTA of a pair ends before the other's last arrival at it.
+    if constexpr (PAIR) cluster_sync();
     if (warp == 0) {
         fence_after_sync();
-        tmem_free(tm, TM_COLS);
+        if constexpr (PAIR) tmem_free_pair(tm, TM_COLS);
+        else tmem_free(tm, TM_COLS);
     }
 }
 
@@ -1175,12 +1240,13 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
     // The parts: slot 2 cta + 1, then slots 2 i of the CTAs after it up to the one that ends
     // the item.  None between is without a part: CTAs with nothing to do come last.
     const Desc d = p.desc[cta];
-    int last = cta;
-    for (int i0 = cta + 1; i0 < n_cta; i0 += 32) {
-        const int i = i0 + lane;
+    // (The CTAs of one rank of the pairs, where they work in pairs.)
+    int n_part = 1;
+    for (int k0 = 1; cta + k0 * p.pair < n_cta; k0 += 32) {
+        const int i = cta + (k0 + lane) * p.pair;
         const uint32_t ends = __ballot_sync(kFullMask, i < n_cta && p.desc[i].head == 2);
         if (ends) {
-            last = i0 + __ffs(ends) - 1;
+            n_part = k0 + __ffs(ends);
             break;
         }
     }
@@ -1198,16 +1264,16 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) attn_paged_combine(const A
                                               grow * p.a.gate_stride + gh * D + 4 * c4);
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = cta; i0 <= last; i0 += 4) {
+        for (int k0 = 0; k0 < n_part; k0 += 4) {
             float2 ml[4];
             float4 a[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int i = min(i0 + k, last);
+                const int i = cta + min(k0 + k, n_part - 1) * p.pair;
                 const size_t slot = 2 * i + (i == cta);
                 ml[k] = __ldg(reinterpret_cast<const float2 *>(p.part_ml) + slot * ROWS + r);
                 a[k] = __ldg(reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + c4) * ROWS + r);
-                if (i0 + k > last) ml[k].x = -INFINITY;
+                if (k0 + k >= n_part) ml[k].x = -INFINITY;
             }
             const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
             if (top == -INFINITY) continue;
@@ -1248,10 +1314,10 @@ constexpr size_t WS_DESC = 256;
 size_t ws_ml(int n_cta) { return WS_DESC + (((size_t)n_cta * sizeof(Desc) + 255) & ~(size_t)255); }
 size_t ws_o(int n_cta) { return ws_ml(n_cta) + (size_t)2 * n_cta * ROWS * 2 * 4; }
 
-template <bool E4M3, bool OUT_BF16>
+template <bool E4M3, bool PAIR, bool OUT_BF16>
 cudaError_t launch_attn(const AttnParams &p, int dev, int n_cta, cudaStream_t s) {
     using L = Layout<E4M3>;
-    const auto kern = attn_paged_kernel<E4M3, OUT_BF16>;
+    const auto kern = attn_paged_kernel<E4M3, PAIR, OUT_BF16>;
     cudaError_t e = cudaSuccess;
     // The kernel's shared-memory limit, raised once per device (setting it twice is harmless).
     static std::atomic<uint64_t> raised{0};
@@ -1264,18 +1330,22 @@ cudaError_t launch_attn(const AttnParams &p, int dev, int n_cta, cudaStream_t s)
         }
         raised.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n_cta);
     cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = L::S_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = PAIR ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e == cudaSuccess) {
+        cfg.numAttrs = 1;
         cfg.gridDim = dim3((unsigned)(n_cta * COMBINE_SPLIT));
         cfg.blockDim = dim3(32 * COMBINE_WARPS);
         cfg.dynamicSmemBytes = 0;
@@ -1303,11 +1373,18 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
     p.a = *a;
     p.shift = log2_of(c.page_size);
     p.n_rep = a->H_q / c.H_kv;
-    p.tile_tok = ROWS / p.n_rep;
+    p.cta_tok = ROWS / p.n_rep;
+    // In pairs where a sequence's new tokens fill a pair's 256 rows on average: each CTA then
+    // loads half of every tile.
+    const bool pair = c.kv_dtype == GDR_BF16 && a->n_tok * p.n_rep >= (int64_t)2 * ROWS * c.n_seq;
+    p.pair = pair ? 2 : 1;
+    p.tile_tok = p.cta_tok * p.pair;
+    const int n_cta = n_sm / p.pair * p.pair;
     p.rep_inv = (65536u + p.n_rep - 1) / p.n_rep;
     const bool codes = c.kv_dtype == GDR_E4M3;
-    p.k_rows = c.page_size < KEYS ? c.page_size : KEYS;
-    const int v_keys = codes ? KEYS : KEYS / 2;  // keys of a V slot
+    const int k_keys = pair ? KEYS / 2 : KEYS;           // keys of a K slot
+    const int v_keys = codes || pair ? KEYS : KEYS / 2;  // of a V slot
+    p.k_rows = c.page_size < k_keys ? c.page_size : k_keys;
     p.v_rows = c.page_size < v_keys ? c.page_size : v_keys;
     p.n_rows = c.n_pages * c.H_kv * c.page_size;
     p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
@@ -1317,15 +1394,18 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
     p.part_ml = reinterpret_cast<float *>(ws + ws_ml(n_sm));
     p.part_o = reinterpret_cast<float *>(ws + ws_o(n_sm));
     const bool maps =
-        encode_bf16_3d(&p.tm_q, a->q, D, a->H_q, a->n_tok, (uint64_t)a->q_stride * 2, 64, p.n_rep, p.tile_tok) &&
+        encode_bf16_3d(&p.tm_q, a->q, D, a->H_q, a->n_tok, (uint64_t)a->q_stride * 2, 64, p.n_rep, p.cta_tok) &&
         (codes ? encode_u8_2d(&p.tm_k, c.k, D, p.n_rows, 128, p.k_rows) &&
                      encode_u8_2d(&p.tm_v, c.v, D, p.n_rows, 128, p.v_rows)
                : encode_bf16_2d(&p.tm_k, c.k, D, p.n_rows, D * 2, 64, p.k_rows) &&
                      encode_bf16_2d(&p.tm_v, c.v, D, p.n_rows, D * 2, 64, p.v_rows));
     if (!maps) return cudaErrorInvalidValue;
     const bool bf16 = a->out_dtype == GDR_BF16;
-    if (codes) return bf16 ? launch_attn<true, true>(p, dev, n_sm, s) : launch_attn<true, false>(p, dev, n_sm, s);
-    return bf16 ? launch_attn<false, true>(p, dev, n_sm, s) : launch_attn<false, false>(p, dev, n_sm, s);
+    if (codes)
+        return bf16 ? launch_attn<true, false, true>(p, dev, n_cta, s) : launch_attn<true, false, false>(p, dev, n_cta, s);
+    if (pair)
+        return bf16 ? launch_attn<false, true, true>(p, dev, n_cta, s) : launch_attn<false, true, false>(p, dev, n_cta, s);
+    return bf16 ? launch_attn<false, false, true>(p, dev, n_cta, s) : launch_attn<false, false, false>(p, dev, n_cta, s);
 }
 
 }  // namespace gdr
