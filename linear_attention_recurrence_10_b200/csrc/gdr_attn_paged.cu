@@ -321,6 +321,24 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint64_
     return done || wait_on(bar, parity, limit);
 }
 
+// The same by looking again and again: for a barrier at which another CTA arrives (a waiting
+// thread that the hardware has suspended is woken late by that: by up to 2000 clocks here).
+__device__ __noinline__ bool spin_on(uint64_t *bar, uint32_t parity) {
+    const uint64_t start = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 255) == 0 && global_ns() - start > kWaitNs) return false;
+    }
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -698,7 +716,10 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 else commit(smem_u32(bar));
             };
             auto landed = [&](int u) {  // in both CTAs of a pair
-                return full_wait(u) && (!PAIR || wait_bar(peer_full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u));
+                return full_wait(u) && (!PAIR || spin_on(peer_full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u));
+            };
+            auto wait_both = [&](uint64_t *bar, uint32_t parity) {  // for arrivals from both CTAs of a pair
+                return PAIR ? spin_on(bar, parity) : wait_bar(bar, parity);
             };
             bool ok = true;
             int jt = 0, base = 0, n_item = 0;
@@ -756,16 +777,16 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 if (it.n_kv == 0) continue;
                 const int n = it.b - it.a;
                 ok = wait_bar(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u) &&
-                     (!PAIR || wait_bar(peer_q, (uint32_t)n_item & 1u)) && score(jt, base + use_k<SPT>(0));
+                     (!PAIR || spin_on(peer_q, (uint32_t)n_item & 1u)) && score(jt, base + use_k<SPT>(0));
                 if (n == 1 && ok) done(q_free);
                 for (int i = 0; i < n && ok; ++i) {
                     if (i + 1 < n) {
                         ok = score(jt + i + 1, base + use_k<SPT>(i + 1));
                         if (i + 2 == n && ok) done(q_free);
                     }
-                    if (ok && i == 0 && n_item > 0) ok = wait_bar(o_free, (uint32_t)(n_item - 1) & 1u);
+                    if (ok && i == 0 && n_item > 0) ok = wait_both(o_free, (uint32_t)(n_item - 1) & 1u);
                     const int j = jt + i, u0 = base + use_v<SPT>(i, n);
-                    ok = ok && wait_bar(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u);
+                    ok = ok && wait_both(bar_p + (j & 1), (uint32_t)(j >> 1) & 1u);
                     const int keys = min(KEYS, it.end - (it.a + i) * KEYS);
                     const uint32_t pt = tm + TM_S + 128 * (j & 1);
 #pragma unroll 1
@@ -1077,6 +1098,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         }
                     }
                     fence_smem_to_async();
+                    if (PAIR) fence_cluster();
                 }
                 fence_before_sync();
                 __syncwarp();

@@ -167,14 +167,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// An arrival on the barrier at this offset in CTA `rank` of the cluster.
+// An arrival on the barrier at this offset in CTA `rank` of the cluster.  It orders what
+// this thread has completed (its tensor memory stores, its waits); ordinary writes that the other
+// CTA is to see take fence_cluster() before it.  (A release at cluster scope in the arrival itself
+// measured 1000 clocks.)
 __device__ __forceinline__ void mbar_arrive_at(uint64_t *bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar)),
         "r"(rank)
         : "memory");
 }
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
