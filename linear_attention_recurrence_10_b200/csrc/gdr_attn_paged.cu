@@ -941,6 +941,15 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 continue;
             }
             const int n = it.b - it.a;
+            const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
+            if (whole && mine && p.a.gate) {
+                // The row's gates come into L2 while its keys are worked on.
+                const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride +
+                                         gh * D + COLS * part;
+#pragma unroll
+                for (int x = 0; x < COLS; x += 64)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(g + x));
+            }
             float m_ref = -INFINITY, l = 0.f;
             float row_factor = 1.f;
             for (int i = 0; i < n; ++i) {
@@ -1112,7 +1121,6 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             l *= E4M3 ? 256.f : 1.f;  // 2^kShift
             group_sync_or(1 + quad, NG, false);  // every maximum has been read
             red[part * 32] = l;
-            const bool begins = it.a == 0, ends = it.b == it.n_kv, whole = begins && ends;
             // For accesses of 32 bytes a row, 16 a lane: the two rows of this lane's pair.
             using T = std::conditional_t<OUT_BF16, __nv_bfloat16, float>;
             constexpr int PER = 16 / sizeof(T);  // values in 16 bytes
