@@ -54,8 +54,10 @@ using namespace gdr::tc;
 
 constexpr int ROWS = 128;  // query rows per item
 constexpr int KEYS = 128;  // keys per tile
-// Cost of starting and finishing an item, in tiles.
-constexpr int ITEM_COST = 2;
+// Cost of starting and finishing an item, in tiles: for the items of a sequence with few new
+// rows, and for others, whose output, gates and sums are most of it.  Four prompts of 4096
+// tokens: 609 us with 2, 563 with 4, 571 with 6; 64 sequences' decode step 106 us with 2, 110 with 4.
+constexpr int FEW_ROWS = 32, COST_FEW = 2, COST_MANY = 4;
 constexpr int AUX_WARPS = 2;      // split Q, prepare scales: code caches only
 constexpr int NRAW = 4;       // tiles of key and value scales in flight
 constexpr uint32_t TM_O = 0, TM_S = 256, TM_COLS = 512;
@@ -146,10 +148,12 @@ __device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
 // A sequence's lengths as the kernels use them.
 struct Seq {
     int cu0, q, len;  // first packed row, new tokens, tokens before; len -1: lengths not usable
+    int start;        // cost of starting and finishing an item
     // From cu_seqlens[s], cu_seqlens[s + 1] and cache_len[s].
     __device__ __forceinline__ void set(const AttnParams &p, int begin, int end, int before) {
         cu0 = max(begin, 0);
         q = max(min(end, (int)p.a.n_tok) - cu0, 0);
+        start = (int64_t)q * p.n_rep <= FEW_ROWS ? COST_FEW : COST_MANY;
         len = before;
         const int64_t total = (int64_t)len + q;
         if (len < 0 || total > ((int64_t)p.a.pages.table_width << p.shift) || total > 0x7fffff00LL) len = -1;
@@ -169,7 +173,7 @@ struct Seq {
     }
     // Cost of the first m query tiles of one kv head.
     __device__ __forceinline__ int64_t cost(const AttnParams &p, int m) const {
-        int64_t u = (int64_t)m * ITEM_COST;
+        int64_t u = (int64_t)m * start;
         if (len < 0 || m == 0) return u;
         const int whole = min(m, q / p.tile_tok);
         u += floor_sum(whole, KEYS, p.tile_tok, (int64_t)len + p.tile_tok + KEYS - 1);
@@ -236,9 +240,9 @@ struct Walk {
             it.end = q.len + min(first + p.tile_tok, q.q);
             it.n_kv = q.keys(p, w.i);
             const bool begins = w.u >= 0;
-            it.a = min(max(-w.u - ITEM_COST, 0), it.n_kv);
-            it.b = min(max(w.len - w.u - ITEM_COST, 0), it.n_kv);
-            w.u += ITEM_COST + it.n_kv;
+            it.a = min(max(-w.u - q.start, 0), it.n_kv);
+            it.b = min(max(w.len - w.u - q.start, 0), it.n_kv);
+            w.u += q.start + it.n_kv;
             ++w.i;
             if (it.a < it.b || (it.n_kv == 0 && begins)) return true;
         }
