@@ -444,8 +444,9 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspac
  *                    gdr_kv_gather the tokens read).  Empty sequences are
  *                    allowed.  Packed rows from cu_seqlens[n_seq] on belong to
  *                    no sequence: they are not read and keep what they hold.
- *   Supported: d = 256; page_size a power of two, 16 .. 1024; n_pages * H_kv *
- *   page_size < 2^31 rows; n_tok < 2^31 - 128 (else GDR_ERR_UNSUPPORTED).
+ *   Supported: d = 256; page_size a power of two, 16 .. 1024; H_kv and H_q at
+ *   most 65535; n_pages * H_kv * page_size and n_tok less than 2^31 - 128 (else
+ *   GDR_ERR_UNSUPPORTED).
  *
  * Nothing about the lengths is read on the host, so a captured graph may be
  * replayed with other lengths in the same arrays.  What only the device can
@@ -532,7 +533,8 @@ gdr_status gdr_kv_gather(const gdr_kv_gather_args *args, gdr_stream_t stream);
  *   out        [n_tok, H_q, d] out_dtype, row stride out_stride
  *   lse        [n_tok, H_q] fp32, row stride lse_stride (0 = H_q), or NULL
  *   scale      positive and finite (d^-1/2 for standard attention)
- *   Supported: H_q a multiple of H_kv with H_q / H_kv <= 128.
+ *   Supported: H_q a multiple of H_kv with H_q / H_kv <= 128.  out and lse overlap
+ *   none of the inputs.
  *   q and the cached rows below a sequence's length must be finite, and v_scale
  *   not negative (less than 2^-40 counts as that); what pages hold past the
  *   length does not matter.

@@ -18,6 +18,7 @@ kernels.  PyTorch is used for device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 
@@ -481,6 +482,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_no_change = contextlib.nullcontext()
+
+
+def _made_current(index):
+    """A context in which CUDA device `index` is the current one (a CPU's -1: no change)."""
+    return _no_change if index < 0 or index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
 def _queue(f, name, packed, more, stream, *tensors):
     """Call library function f on one device's stream: all tensors' device, made current."""
     index = tensors[0].get_device()
@@ -491,10 +500,7 @@ def _queue(f, name, packed, more, stream, *tensors):
         handle = _raw_stream(index) if index >= 0 else 0
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index >= 0 and index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            status = f(packed, *more, handle)
-    else:
+    with _made_current(index):
         status = f(packed, *more, handle)
     if status:
         raise GdrError(status, name)
@@ -605,8 +611,9 @@ def attn_paged_workspace_size(q, k_pages, v_pages, page_table, cu_seqlens, cache
     a = _attn_paged_args(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, k_scale,
                          v_scale, gate, lse, scale)
     n = ctypes.c_size_t(0)
-    _check(_abi.lib().gdr_attn_paged_workspace_size(a, ctypes.byref(n)),
-           "gdr_attn_paged_workspace_size")
+    with _made_current(q.get_device()):
+        _check(_abi.lib().gdr_attn_paged_workspace_size(a, ctypes.byref(n)),
+               "gdr_attn_paged_workspace_size")
     return int(n.value)
 
 
@@ -629,9 +636,14 @@ def attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *, k
     L = _abi.lib()
     if workspace is None:
         n = ctypes.c_size_t(0)
-        _check(L.gdr_attn_paged_workspace_size(a, ctypes.byref(n)), "gdr_attn_paged_workspace_size")
+        with _made_current(q.get_device()):
+            _check(L.gdr_attn_paged_workspace_size(a, ctypes.byref(n)),
+                   "gdr_attn_paged_workspace_size")
         if n.value:
             workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+            if stream is not None and q.is_cuda:  # it is not reused before that stream is done with it
+                workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
+                                        torch.cuda.ExternalStream(int(stream), device=q.device))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _queue(L.gdr_attn_paged, "gdr_attn_paged", a, (_ptr0(workspace), ws_bytes), stream, q, k_pages,
            v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale, gate, lse, workspace)

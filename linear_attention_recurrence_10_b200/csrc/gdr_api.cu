@@ -477,9 +477,9 @@ static gdr_status pages_check(gdr_kv_pages *g, int64_t n_tok) {
     if (g->d != 256) return GDR_ERR_UNSUPPORTED;
     if (g->page_size < 16 || g->page_size > 1024 || (g->page_size & (g->page_size - 1)))
         return GDR_ERR_UNSUPPORTED;
-    // Cache rows and packed rows are addressed with 32-bit signed coordinates.
-    if (g->H_kv > 0x7fffffff / g->page_size ||
-        (int64_t)g->H_kv * g->page_size * g->n_pages > 0x7fffffffLL)
+    // Cache rows and packed rows are addressed with 32-bit signed coordinates, a box of
+    // rows past the last one among them.
+    if (g->H_kv > 65535 || (int64_t)g->H_kv * g->page_size * g->n_pages > 0x7fffffffLL - 128)
         return GDR_ERR_UNSUPPORTED;
     if (n_tok > 0x7fffffffLL - 128) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
@@ -502,7 +502,7 @@ static gdr_status attn_paged_check(gdr_attn_paged_args *a) {
     if (a->H_q <= 0 || a->reserved != 0 || !dtype_ok(a->out_dtype)) return GDR_ERR_INVALID_ARG;
     if (a->H_q % a->pages.H_kv != 0) return GDR_ERR_INVALID_ARG;
     if (!(a->scale > 0.f) || !(a->scale <= 3.4028235e38f)) return GDR_ERR_INVALID_ARG;
-    if (a->H_q / a->pages.H_kv > 128) return GDR_ERR_UNSUPPORTED;
+    if (a->H_q > 65535 || a->H_q / a->pages.H_kv > 128) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
 }
 
@@ -517,6 +517,7 @@ gdr_status gdr_kv_append(const gdr_kv_append_args *args, gdr_stream_t stream) {
     if (!(a.rope_theta > 0.f) || !(a.rope_theta <= 3.4028235e38f)) return GDR_ERR_INVALID_ARG;
     if (!a.q != !a.q_out || (a.H_q > 0 && !a.q && a.n_tok > 0) || (a.H_q == 0 && a.q))
         return GDR_ERR_INVALID_ARG;
+    if (a.H_q > 65535) return GDR_ERR_UNSUPPORTED;
     const int64_t d = a.pages.d;
     GDR_TRY(resolve_stride(a.q_stride, a.H_q * d, 2, &a.q_stride));
     GDR_TRY(resolve_stride(a.q_out_stride, a.H_q * d, 2, &a.q_out_stride));

@@ -83,7 +83,8 @@ PAGES = [
     ("page_0", dict(page_size=0), INVALID),
     ("negative_pages", dict(n_pages=-1), INVALID),
     ("rows_past_int32", dict(n_pages=1 << 25), UNSUPPORTED),
-    ("heads_past_int32", dict(H_kv=1 << 26, H_q=1 << 26), UNSUPPORTED),
+    ("too_many_heads", dict(H_kv=1 << 16, H_q=1 << 16), UNSUPPORTED),
+    ("rows_at_int32", dict(H_kv=1, H_q=1, page_size=1024, n_pages=1 << 21), UNSUPPORTED),
     ("fp32_cache", dict(kv_dtype=0), INVALID),
     ("unknown_cache_type", dict(kv_dtype=3), INVALID),
     ("scales_with_bf16", dict(kv_dtype=1), INVALID),

@@ -241,6 +241,56 @@ def test_attend_chunks(new, past, kind):
     p.check_attend(out, lse)
 
 
+@pytest.mark.parametrize("heads,page", list(zip(HEADS + [(128, 1), (10, 1)], [32, 64, 16, 128, 1024, 256, 16])))
+def test_attend_long_chunks(heads, page):
+    """New tokens that fill 256 rows and more per key head, over a bf16 cache (the tiles are then
+    shared by two thread blocks): lengths that leave the second one few rows, none, and few keys."""
+    rep = heads[0] // heads[1]
+    big = -(-700 // rep)
+    p = Problem(new=[big, 3 + 128 // rep, big + 5, 1], past=[0, 77, 130, 40], H_q=heads[0], H_kv=heads[1],
+                page=page, seed=300 + page, tail=3)
+    assert p.rows * rep >= 256 * p.n_seq  # the rule for it
+    p.put_plain()
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse, ws = p.attend(out_dtype=dtype)
+        assert status_of(ws) == 0
+        p.check_attend(out, lse)
+
+
+@pytest.mark.parametrize("fault", ["page", "length"])
+def test_attend_long_chunks_bad_pages(fault):
+    p = Problem(new=[200, 200, 200], past=[10, 20, 30], page=32, seed=310)
+    p.put_plain()
+    good = p.table.clone(), p.cache_len.clone()
+    if fault == "page":
+        p.table[1, 3] = -1
+    else:
+        p.cache_len[1] = 1 << 30
+    out, lse, ws = p.attend()
+    assert status_of(ws) == 1
+    p.table, p.cache_len = good
+    out[200:400] = 0
+    p.check_attend(out, lse, only=(0, 2))
+
+
+def test_attend_allocates_its_workspace_for_the_stream():
+    """No workspace given, on a stream of its own: what is allocated is not handed out again
+    while the call may still run."""
+    p = Problem(new=[300], past=[3000], page=64, seed=320)
+    p.put_plain()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(6):
+        out = torch.empty_like(p.q)
+        gdr.attn_paged(p.q, *p.pages, p.cache_len, out, gate=p.gate, stream=s)
+        torch.empty(39 << 20, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        outs.append(out)
+    torch.cuda.synchronize()
+    for out in outs:
+        p.check_attend(out, None)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_attend_options(kind):
     """fp32 output, no gate, no lse, another scale; strided q, gate, out, lse and table."""
