@@ -24,6 +24,13 @@
 // sum, write P over S in tensor memory and rescale O when the maximum has moved
 // far.  S of the next tile is computed while the softmax works on this one.
 //
+// Long chunks over a bf16 cache go by pairs of CTAs: alone, a CTA's 128 rows use each
+// 128 KB tile of keys and values for 16.8 MFLOP, and the L2 cache cannot feed 148 of
+// them (2970 clocks a tile, a third of them waiting for loads).  The two CTAs of a cluster
+// take 256 rows and load half of every tile each (cta_group::2 multiplies both halves
+// for both): no wait for loads is left, and a tile takes 2500 clocks, of which the
+// products are 2048 and the rest the round from S through the softmax back to P V.
+//
 // A code cache is multiplied as it is, in e4m3, at twice bf16's rate and with
 // nothing to convert: the other operand is split in two e4m3 parts, x ~ hi + lo,
 // which hold 8 significant bits as bf16 does.  Q (bf16) times a power of two
@@ -32,6 +39,20 @@
 // weights, w_j = 2^(a_j + log2 sv_j - m), which P holds, with the maximum taken
 // over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Two more warps split
 // Q and prepare the scales.
+//
+// What bounds it, 16 query heads over 2 key/value heads:
+//   decode, 64 sequences of 4096 tokens: bf16, 107 us, the 0.54 GB of the cache at 5.0 TB/s;
+//     codes, 90 us (0.27 GB, 3.0 TB/s): the products, 3100 clocks a tile with operands from shared
+//     memory, 128 rows of which 8 are wanted, against 2800 for a tile's bytes.  Spreading those
+//     8 rows' softmax over all warps brought nothing.
+//   2048 tokens after 6144, bf16: 228 us, 1.06 PFLOP/s with clocks near 1.5 GHz under the
+//     power limit (200 us, 1.2 PFLOP/s, alone on a cool card).
+//   4 prompts of 4096, bf16: 565 us, 0.97 PFLOP/s; of that the output gates are 85 us: an
+//     exponential and half a reciprocal a value, while nothing is multiplied.
+//   the same by codes: the softmax of a tile, 3900 clocks, four threads a row and three
+//     times bf16's instructions a key (scales, two parts).
+// P in shared memory with S two tiles ahead (pairs) measured 238 us for 232: P's one buffer
+// then makes the softmax wait for P V.
 //
 // Every wait is bounded (2 s); on expiry a role records GDR_ERR_TIMEOUT, the
 // others run into their own limits, copies and commits in flight are waited
@@ -73,9 +94,9 @@ constexpr uint32_t BOX = 16384;
 template <bool E4M3>
 struct Layout {
     // Threads that share a row, each with KEYS / PARTS keys of a tile.  Codes take four:
-    // their weights cost three times bf16's instructions, and the split of each row over more
-    // warps hides more of the latency than the smaller register share costs.  bf16 at four:
-    // 3300 clocks a tile instead of 2970, the MMA thread's warp having less of its scheduler.
+    // their weights cost three times bf16's instructions, and more warps hide more of the
+    // latency than their smaller register share costs (a tile: 4400 clocks with two, 3900).
+    // bf16 at four: 3300 clocks instead of 2970, the MMA thread having less of its scheduler.
     static constexpr int PARTS = E4M3 ? 4 : 2;
     static constexpr int SOFTMAX = 4 * PARTS;  // softmax warps: 0 ..
     static constexpr int W_LOAD = SOFTMAX, W_MMA = SOFTMAX + 1, W_AUX = SOFTMAX + 2;
@@ -1408,8 +1429,9 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
     p.shift = log2_of(c.page_size);
     p.n_rep = a->H_q / c.H_kv;
     p.cta_tok = ROWS / p.n_rep;
-    // In pairs where a sequence's new tokens fill a pair's 256 rows on average: each CTA then
-    // loads half of every tile.
+    // In pairs where a sequence's new tokens fill a pair's 256 rows on average, which is as much
+    // as the host knows: a chunk of 2048 tokens takes 228 us so and 253 alone, while of a decode
+    // step's 8 rows a pair would give one CTA none.
     const bool pair = c.kv_dtype == GDR_BF16 && a->n_tok * p.n_rep >= (int64_t)2 * ROWS * c.n_seq;
     p.pair = pair ? 2 : 1;
     p.tile_tok = p.cta_tok * p.pair;
