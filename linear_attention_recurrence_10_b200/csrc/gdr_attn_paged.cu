@@ -109,7 +109,7 @@ struct Layout {
     static constexpr uint32_t S_RING = 4 * BOX;
     static constexpr uint32_t S_RED = S_RING + NSLOT * SLOT;         // [4 quads][2][PARTS][32] floats
     static constexpr uint32_t S_SCALE = S_RED + 1024 * PARTS;  // [2][3][128] floats
-    static constexpr uint32_t S_RAW = S_SCALE + (E4M3 ? 3072 : 0);   // [NRAW][2][128] floats
+    static constexpr uint32_t S_RAW = S_SCALE + (E4M3 ? 6 * 512 : 0);   // [NRAW][2][128] floats
     static constexpr uint32_t S_ROWK = S_RAW + (E4M3 ? NRAW * 1024 : 0);  // [2][128] floats
     static constexpr uint32_t S_BAR = S_ROWK + (E4M3 ? 1024 : 0);
     static constexpr uint32_t S_BYTES = S_BAR + 544;
