@@ -535,6 +535,50 @@ def test_captured_step_replayed_with_other_lengths(kind):
     del graph
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_captured_chunk_replayed_beside_eager_calls(kind):
+    """A captured chunk (paired over bf16) replayed with other lengths, between eager calls on
+    another stream with a workspace of their own."""
+    p = Problem(new=[300, 200], past=[100, 900], page=64, kind=kind, seed=260, spare=8)  # holds every case
+    p.put_plain()
+    other = Problem(new=[77], past=[400], page=64, kind=kind, seed=261)
+    other.put_plain()
+    out, lse = torch.empty_like(p.q), torch.empty(p.rows, 16, device="cuda")
+    args = (p.q, *p.pages, p.cache_len, out)
+    kw = dict(**p.scales, gate=p.gate, lse=lse)
+    ws = torch.empty(gdr.attn_paged_workspace_size(*args, **kw), dtype=torch.uint8, device="cuda")
+    gdr.attn_paged(*args, **kw, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdr.attn_paged(*args, **kw, workspace=ws)
+    side = torch.cuda.Stream()
+    for new, past in (([300, 200], [100, 900]), ([450, 50], [0, 1050]), ([0, 500], [5, 600])):
+        p.new, p.past, p.len = new, past, [a + b for a, b in zip(new, past)]
+        q = Problem(new=new, past=past, page=64, kind=kind, seed=262, width=p.width)
+        q.put_plain()
+        assert q.n_pages <= p.n_pages
+        for n in ("k_pages", "v_pages", "k_scale", "v_scale"):
+            if getattr(p, n) is not None:
+                getattr(p, n)[:q.n_pages].copy_(getattr(q, n))
+        for n in ("q", "gate", "table", "cu", "cache_len"):
+            getattr(p, n).copy_(getattr(q, n))
+        out.fill_(NAN)
+        lse.fill_(NAN)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            first = other.attend()
+        graph.replay()
+        with torch.cuda.stream(side):
+            second = other.attend()
+        torch.cuda.synchronize()
+        assert status_of(ws) == 0
+        p.check_attend(out, lse)
+        assert torch.equal(first[0], second[0])
+        other.check_attend(*first[:2])
+    del graph
+
+
 def test_two_streams_at_once():
     """Two calls in flight, each on its own stream with its own workspace."""
     ps = [Problem(new=[200, 1], past=[100 * i, 2000], page=64, kind=k, seed=240 + i)
