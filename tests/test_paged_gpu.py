@@ -241,14 +241,15 @@ def test_attend_chunks(new, past, kind):
     p.check_attend(out, lse)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,page", list(zip(HEADS + [(128, 1), (10, 1)], [32, 64, 16, 128, 1024, 256, 16])))
-def test_attend_long_chunks(heads, page):
-    """New tokens that fill 256 rows and more per key head, over a bf16 cache (the tiles are then
-    shared by two thread blocks): lengths that leave the second one few rows, none, and few keys."""
+def test_attend_long_chunks(heads, page, kind):
+    """New tokens that fill 256 rows and more per key head (the tiles are then shared by two
+    thread blocks): lengths that leave the second one few rows, none, and few keys."""
     rep = heads[0] // heads[1]
     big = -(-700 // rep)
     p = Problem(new=[big, 3 + 128 // rep, big + 5, 1], past=[0, 77, 130, 40], H_q=heads[0], H_kv=heads[1],
-                page=page, seed=300 + page, tail=3)
+                page=page, kind=kind, seed=300 + page, tail=3)
     assert p.rows * rep >= 256 * p.n_seq  # the rule for it
     p.put_plain()
     for dtype in (torch.bfloat16, torch.float32):
@@ -257,9 +258,10 @@ def test_attend_long_chunks(heads, page):
         p.check_attend(out, lse)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("fault", ["page", "length"])
-def test_attend_long_chunks_bad_pages(fault):
-    p = Problem(new=[200, 200, 200], past=[10, 20, 30], page=32, seed=310)
+def test_attend_long_chunks_bad_pages(fault, kind):
+    p = Problem(new=[200, 200, 200], past=[10, 20, 30], page=32, kind=kind, seed=310)
     p.put_plain()
     good = p.table.clone(), p.cache_len.clone()
     if fault == "page":
@@ -537,7 +539,7 @@ def test_captured_step_replayed_with_other_lengths(kind):
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_captured_chunk_replayed_beside_eager_calls(kind):
-    """A captured chunk (paired over bf16) replayed with other lengths, between eager calls on
+    """A captured chunk (of paired blocks) replayed with other lengths, between eager calls on
     another stream with a workspace of their own."""
     p = Problem(new=[300, 200], past=[100, 900], page=64, kind=kind, seed=260, spare=8)  # holds every case
     p.put_plain()
