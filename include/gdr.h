@@ -443,7 +443,8 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspac
  *                    the call's packed tensors (its new tokens; for
  *                    gdr_kv_gather the tokens read).  Empty sequences are
  *                    allowed.  Packed rows from cu_seqlens[n_seq] on belong to
- *                    no sequence: they are not read and keep what they hold.
+ *                    no sequence: what inputs hold there does not matter, and
+ *                    outputs keep what they hold.
  *   Supported: d = 256; page_size a power of two, 16 .. 1024; H_kv and H_q at
  *   most 65535; n_pages * H_kv * page_size and n_tok less than 2^31 - 128 (else
  *   GDR_ERR_UNSUPPORTED).
