@@ -1041,6 +1041,33 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 }
                 dead = group_sync_or(1 + quad, NG, !ok || fault);
                 if (dead) break;
+                // The MMA takes V's keys in steps of 16 (32 codes): what pages hold between
+                // the sequence's end and the step's becomes zero.  (Here, and not just before P's
+                // arrival: 64 x 4096 over codes 89.2 instead of 91.1 us.)
+                const int keys = it.end - k0;
+                constexpr int STEP = E4M3 ? 32 : 16;
+                if (keys < KEYS && (keys & (STEP - 1))) {
+                    const int up = (keys + STEP - 1) & ~(STEP - 1);
+                    // 16 bytes each: bf16, 4 boxes of 8 a key; pairs, 2 boxes; codes, 2 slots.
+                    constexpr int CH = E4M3 || PAIR ? 16 : 32;
+                    constexpr uint32_t COL = PAIR ? BOX : BOX / 2;
+                    const int u0 = base + use_v<SPT>(i, n);
+                    const int u = E4M3 || PAIR ? u0 : u0 + (keys >> 6);
+                    bool okv = full_wait(u);
+                    if (E4M3) okv = okv && full_wait(u0 + 1);
+                    fault = fault || !__all_sync(kFullMask, okv);
+                    if (!fault) {
+                        for (int x = tid; x < (up - keys) * CH; x += 32 * L::SOFTMAX) {
+                            const int key = keys + x / CH, ch = x % CH;
+                            const int uu = E4M3 ? u0 + (ch >> 3) : u;
+                            const uint32_t at = ring + (uu % NSLOT) * L::SLOT + (E4M3 ? 0 : (ch >> 3) * COL) +
+                                                (E4M3 || PAIR ? key : key & 63) * 128 + (ch & 7) * 16;
+                            st_shared16(at, make_uint4(0, 0, 0, 0));
+                        }
+                    }
+                    fence_smem_to_async();
+                    if (PAIR) fence_cluster();
+                }
                 if (some) {
                     top = -INFINITY;
 #pragma unroll
@@ -1094,7 +1121,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     }
                     l += (l2.x + l2.y) + (l3.x + l3.y);
                     if (rescale) {
-                        fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs));
+                        fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs)) || fault;
                         if (!fault) {
                             fence_after_sync();
 #pragma unroll 1
@@ -1107,32 +1134,6 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                             }
                         }
                     }
-                }
-                // The MMA takes V's keys in steps of 16 (32 codes): what pages hold between
-                // the sequence's end and the step's becomes zero.
-                const int keys = it.end - k0;
-                constexpr int STEP = E4M3 ? 32 : 16;
-                if (keys < KEYS && (keys & (STEP - 1))) {
-                    const int up = (keys + STEP - 1) & ~(STEP - 1);
-                    // 16 bytes each: bf16, 4 boxes of 8 a key; pairs, 2 boxes; codes, 2 slots.
-                    constexpr int CH = E4M3 || PAIR ? 16 : 32;
-                    constexpr uint32_t COL = PAIR ? BOX : BOX / 2;
-                    const int u0 = base + use_v<SPT>(i, n);
-                    const int u = E4M3 || PAIR ? u0 : u0 + (keys >> 6);
-                    bool okv = full_wait(u);
-                    if (E4M3) okv = okv && full_wait(u0 + 1);
-                    fault = fault || !__all_sync(kFullMask, okv);
-                    if (!fault) {
-                        for (int x = tid; x < (up - keys) * CH; x += 32 * L::SOFTMAX) {
-                            const int key = keys + x / CH, ch = x % CH;
-                            const int uu = E4M3 ? u0 + (ch >> 3) : u;
-                            const uint32_t at = ring + (uu % NSLOT) * L::SLOT + (E4M3 ? 0 : (ch >> 3) * COL) +
-                                                (E4M3 || PAIR ? key : key & 63) * 128 + (ch & 7) * 16;
-                            st_shared16(at, make_uint4(0, 0, 0, 0));
-                        }
-                    }
-                    fence_smem_to_async();
-                    if (PAIR) fence_cluster();
                 }
                 fence_before_sync();
                 __syncwarp();
