@@ -1046,7 +1046,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 // arrival: 64 x 4096 over codes 89.2 instead of 91.1 us.)
                 const int keys = it.end - k0;
                 constexpr int STEP = E4M3 ? 32 : 16;
-                if (keys < KEYS && (keys & (STEP - 1))) {
+                const bool clears = keys < KEYS && (keys & (STEP - 1));
+                if (clears) {
                     const int up = (keys + STEP - 1) & ~(STEP - 1);
                     // 16 bytes each: bf16, 4 boxes of 8 a key; pairs, 2 boxes; codes, 2 slots.
                     constexpr int CH = E4M3 || PAIR ? 16 : 32;
@@ -1066,7 +1067,6 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         }
                     }
                     fence_smem_to_async();
-                    if (PAIR) fence_cluster();
                 }
                 if (some) {
                     top = -INFINITY;
@@ -1137,7 +1137,12 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 }
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive_mma(bar_p + (j & 1));
+                if (lane == 0) {
+                    // The whole warp's zeros, which the barrier above has brought to this lane,
+                    // before its arrival at the other CTA.
+                    if (PAIR && clears) fence_cluster();
+                    arrive_mma(bar_p + (j & 1));
+                }
             }
             if (dead) break;
             jt += n;
