@@ -78,6 +78,25 @@ def _stream(stream, device) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _workspace(n_bytes: int, stream, device) -> torch.Tensor:
+    """A workspace for one call on `stream` (None: the current one).
+
+    It is allocated with that stream as the current one.  The allocator hands a freed block
+    out again in the order of the stream it was allocated on: taken from another stream's,
+    it could still be in use by work queued there, which `stream` does not wait for, and
+    when the call returns it would go back to that stream while this one still uses it.
+    """
+    if stream is not None and device.type == "cuda":
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != torch.cuda.current_stream(device).cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(handle, device=device) if handle else
+                          torch.cuda.default_stream(device))
+            with torch.cuda.stream(stream):
+                return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+
+
 def _f32_tensor(t, what):
     if t is not None and t.dtype != torch.float32:
         raise TypeError(f"{what} must be fp32")
@@ -640,10 +659,7 @@ def attn_paged(q, k_pages, v_pages, page_table, cu_seqlens, cache_len, out, *, k
             _check(L.gdr_attn_paged_workspace_size(a, ctypes.byref(n)),
                    "gdr_attn_paged_workspace_size")
         if n.value:
-            workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
-            if stream is not None and q.is_cuda:  # it is not reused before that stream is done with it
-                workspace.record_stream(stream if hasattr(stream, "cuda_stream") else
-                                        torch.cuda.ExternalStream(int(stream), device=q.device))
+            workspace = _workspace(int(n.value), stream, q.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _queue(L.gdr_attn_paged, "gdr_attn_paged", a, (_ptr0(workspace), ws_bytes), stream, q, k_pages,
            v_pages, page_table, cu_seqlens, cache_len, out, k_scale, v_scale, gate, lse, workspace)

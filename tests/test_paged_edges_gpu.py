@@ -29,3 +29,69 @@ def test_last_tiles_of_every_length(kind):
         for _ in range(20):
             again, lse2, _ = p.attend(workspace=ws)
             assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------- workspaces that a call allocates
+
+
+def given_workspace(monkeypatch):
+    """The workspaces' addresses of the calls to come."""
+    seen, queue = [], gdr._queue
+
+    def spy(f, name, packed, more, stream, *tensors):
+        seen.append(more[0] if more else None)
+        return queue(f, name, packed, more, stream, *tensors)
+
+    monkeypatch.setattr(gdr, "_queue", spy)
+    return seen
+
+
+@pytest.mark.parametrize("handle", ["stream", "integer"])
+def test_allocated_workspace_is_not_in_use_elsewhere(monkeypatch, handle):
+    """A call on a stream of its own while the current stream still has work on a block of the
+    workspace's size that has just been freed: the call does not get that block, and neither
+    the call's result nor the block's last values change."""
+    p = Problem(new=[300], past=[3000], page=64, seed=320)
+    p.put_plain()
+    want, _, ws = p.attend()
+    n = ws.numel()
+    del ws
+    seen = given_workspace(monkeypatch)
+    a = torch.randn(8192, 8192, device="cuda", dtype=torch.bfloat16)
+    b, out = torch.empty_like(a), torch.empty_like(p.q)
+    s = torch.cuda.Stream()
+    # (A block of this size comes from no larger one: the pool holds none that is free.)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    for _ in range(3):
+        for _ in range(40):
+            torch.mm(a, a, out=b)
+        block = torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF)
+        at, low = block.data_ptr(), block.amin()
+        del block
+        gdr.attn_paged(p.q, *p.pages, p.cache_len, out, gate=p.gate,
+                       stream=s if handle == "stream" else s.cuda_stream)
+        assert seen[-1] != at
+        torch.cuda.synchronize()
+        assert int(low) == 0xFF and torch.equal(out, want)
+
+
+def test_allocated_workspace_on_the_default_stream_by_its_handle(monkeypatch):
+    """stream=0 is the device's default stream, whichever is current."""
+    p = Problem(new=[40], past=[300], page=64, seed=321)
+    p.put_plain()
+    want, _, ws = p.attend()
+    n, out = ws.numel(), torch.empty_like(p.q)
+    del ws
+    seen = given_workspace(monkeypatch)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        block = torch.empty(n, dtype=torch.uint8, device="cuda")
+        at = block.data_ptr()
+        del block
+        gdr.attn_paged(p.q, *p.pages, p.cache_len, out, gate=p.gate, stream=0)
+    assert seen[-1] != at
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
