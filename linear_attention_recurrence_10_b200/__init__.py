@@ -292,7 +292,7 @@ def prefill_chunked(q, k, v, g, beta, cu_seqlens, out, *, cu_seqlens_host=None, 
     _check(L.gdr_prefill_workspace_size(ctypes.byref(a), ctypes.byref(n)),
            "gdr_prefill_workspace_size")
     if workspace is None and n.value:
-        workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(int(n.value), stream, q.device)
     ws_ptr = _ptr(workspace)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(L.gdr_prefill_chunked(ctypes.byref(a), ws_ptr, ws_bytes, _stream(stream, q.device)),
@@ -405,7 +405,7 @@ def attn_decode_step(q, gate, k, v, k_cache, v_cache, cache_len, out, *, kv_boun
     _check(L.gdr_attn_decode_workspace_size(ctypes.byref(a), ctypes.byref(n)),
            "gdr_attn_decode_workspace_size")
     if workspace is None and n.value:
-        workspace = torch.empty(int(n.value), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(int(n.value), stream, q.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(L.gdr_attn_decode_step(ctypes.byref(a), _ptr(workspace), ws_bytes,
                                   _stream(stream, q.device)), "gdr_attn_decode_step")
@@ -722,7 +722,7 @@ def moe_decode(x, w_router, w_gate_up, w_down, out, *, top_k=8, shared=None, top
     n = ctypes.c_size_t(0)
     _check(L.gdr_moe_workspace_size(ctypes.byref(a), ctypes.byref(n)), "gdr_moe_workspace_size")
     if workspace is None and n.value:
-        workspace = torch.empty(int(n.value), dtype=torch.uint8, device=x.device)
+        workspace = _workspace(int(n.value), stream, x.device)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(L.gdr_moe_decode(ctypes.byref(a), _ptr(workspace), ws_bytes, _stream(stream, x.device)),
            "gdr_moe_decode")
