@@ -515,6 +515,9 @@ def _queue(f, name, packed, more, stream, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError(f"all tensors must be on one device: {tensors[0].device} and {t.device}")
+    # (Without a GPU the library's own checks run, and its launch fails.)
+    if index < 0 and torch.cuda.is_available():
+        raise ValueError(f"{name}: tensors must be on a CUDA device, not {tensors[0].device}")
     if stream is None:
         handle = _raw_stream(index) if index >= 0 else 0
     else:

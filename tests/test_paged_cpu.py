@@ -327,3 +327,21 @@ def test_packed_structs_are_the_declared_ones():
         data = fmt.pack(*values)
         for (offset, t), want in zip(flat, values):
             assert t.from_buffer_copy(data, offset).value == want, (cls.__name__, offset)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_host_tensors_are_refused_where_there_is_a_gpu(monkeypatch, kind):
+    """Tensors in host memory never reach the library on a machine with a GPU (here: a stand-in
+    for the library, and a torch that says it has one)."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                assert name.endswith("workspace_size"), f"{name} was called with host addresses"
+                return OK
+            return call
+
+    monkeypatch.setattr(_abi, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    for name, call in _calls(_tensors(kind)).items():
+        with pytest.raises(ValueError, match=f"{name}.*CUDA device"):
+            call()
