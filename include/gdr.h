@@ -529,7 +529,8 @@ gdr_status gdr_kv_gather(const gdr_kv_gather_args *args, gdr_stream_t stream);
  *     y_h  = (sum_{j <= t} exp(a_j - lse_h) v_g[j]) * sigmoid(gate_h)
  *
  *   q, gate    [n_tok, H_q, d] bf16, row strides q_stride, gate_stride; q as
- *              gdr_kv_append leaves it (rotated); gate NULL for no gate
+ *              gdr_kv_append leaves it (rotated); gate NULL for no gate, of any
+ *              value: -infinity makes its output 0, a NaN makes it NaN
  *   cache_len  device int32 [n_seq]: tokens cached before the new ones
  *   out        [n_tok, H_q, d] out_dtype, row stride out_stride
  *   lse        [n_tok, H_q] fp32, row stride lse_stride (0 = H_q), or NULL

@@ -413,8 +413,10 @@ __device__ __forceinline__ void split2(uint32_t h2, uint16_t &hi, uint16_t &lo) 
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
 }
 // a, b times inv and the sigmoids of two bf16 gates, 1 / (1 + 2^u) with u = -g log2(e): one
-// reciprocal for both, of the product (u is held below 60, where the sigmoid is
-// 2^-60 of what it multiplies).
+// reciprocal for both, of the product, which must not overflow, so u is held below 60
+// (fminf also keeps a NaN out of its neighbour's value).  Right for gates of a magnitude
+// below FAR_GATE (a bf16's bits: 41.75, 2^60.2); rows with others are written again by gate_any.
+constexpr uint32_t FAR_GATE = 0x4227;
 __device__ __forceinline__ void gate2(float &a, float &b, uint32_t gates, float inv) {
     const float2 u = mul2(make_float2(__uint_as_float(gates << 16), __uint_as_float(gates & 0xffff0000u)),
                           make_float2(-1.4426950408889634f, -1.4426950408889634f));
@@ -426,6 +428,12 @@ __device__ __forceinline__ void gate2(float &a, float &b, uint32_t gates, float 
     const float2 y = mul2(make_float2(a, b), mul2(make_float2(d.y, d.x), make_float2(r, r)));
     a = y.x;
     b = y.y;
+}
+// a times the sigmoid of any gate: 0 times a for -inf, NaN for a NaN.
+__device__ __forceinline__ float gate_any(float a, float g) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(g * -1.4426950408889634f)));
+    return a * r;
 }
 // Four weights as e4m3 codes in two parts, with integer instructions: the conversions
 // run at 16 lanes a clock for the SM, like the exponentials beside them.  The weights come
@@ -1187,6 +1195,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             fence_after_sync();
             const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint32_t gate_top = 0;  // magnitudes of the row's gates, by halves of a word
             if (some) {
 #pragma unroll 1
                 for (int x = 0; x < COLS; x += 16) {
@@ -1211,6 +1220,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                             const uint4 c8 = g[y >> 3];
                             const uint32_t w4[4] = {c8.x, c8.y, c8.z, c8.w};
                             gate2(o[y], o[y + 1], w4[(y & 7) >> 1], inv);
+                            gate_top = __vmaxu2(gate_top, w4[(y & 7) >> 1] & 0x7fff7fffu);
                         }
                     } else {
 #pragma unroll
@@ -1234,6 +1244,27 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             if (has[k]) *reinterpret_cast<uint4 *>(out_at[k] + x + y) = q2[k];
+                    }
+                }
+                const bool far = mine && max(gate_top >> 16, gate_top & 0xffffu) >= FAR_GATE;
+                if (__any_sync(kFullMask, far)) {
+                    // (The stores above, by two lanes a row, come before the warp's barrier here.)
+                    const int64_t col = gh * D + COLS * part;
+                    const __nv_bfloat16 *g = static_cast<const __nv_bfloat16 *>(p.a.gate) + grow * p.a.gate_stride + col;
+                    T *to = static_cast<T *>(p.a.out) + grow * p.a.out_stride + col;
+#pragma unroll 1
+                    for (int x = 0; x < COLS; x += 16) {
+                        float o[16];
+                        __syncwarp();
+                        tmem_ld16(tm + lane_off + TM_O + COLS * part + x, o);
+                        if (far)
+#pragma unroll
+                            for (int y = 0; y < 16; y += 4) {
+                                const float4 f = Elem<__nv_bfloat16>::load4(g + x + y);
+                                Elem<T>::store4(to + x + y, make_float4(gate_any(o[y] * inv, f.x), gate_any(o[y + 1] * inv, f.y),
+                                                                        gate_any(o[y + 2] * inv, f.z),
+                                                                        gate_any(o[y + 3] * inv, f.w)));
+                            }
                     }
                 }
                 if (mine && part == 0) {

@@ -95,3 +95,43 @@ def test_allocated_workspace_on_the_default_stream_by_its_handle(monkeypatch):
     assert seen[-1] != at
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ gates
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,past", [([1] * 300, [90] * 300),        # items in one piece, most of them
+                                      ([1, 3], [9000, 20]),           # an item in many pieces
+                                      ([260, 300, 280], [0, 40, 0])])  # (pairs, for bf16)
+def test_gates_of_any_value(kind, new, past):
+    """NaN, infinite and far gates change their own value alone, whether or not the split of
+    the work has cut their item.  Beside the same call without gates, in fp32, an output is off by
+    the sigmoid: u = g log2(e) is rounded twice, |u| <= 128 (2^-24 + 2^-24), its power, the
+    reciprocal and the products add less than 2^-20 in all: 2^-16 relative; below 2^-126 it may
+    be 0.  A bf16 output rounds by U8 relative, and below 2^-126, where bf16's steps are
+    2^-126 2^-7 = 2^-133, by half of one."""
+    p = Problem(new=new, past=past, page=64, kind=kind, seed=420)
+    p.put_plain()
+    plain, _, ws = p.attend(gate=False, out_dtype=torch.float32)
+    assert status_of(ws) == 0
+    p.check_attend(plain, None, gate=False)
+    values = [NAN, float("inf"), -float("inf"), -41.5, -41.75, -50.0, -80.0, -87.5, -100.0, -3e38, 41.75, 60.0,
+              3e38, -NAN, 0.0]
+    g = torch.Generator().manual_seed(421)
+    for share in (0.002, 0.5):  # one of a row's gates, now and then; half of them
+        at = (torch.rand(p.gate.shape, generator=g) < share).cuda()
+        which = torch.randint(0, len(values), p.gate.shape, generator=g).cuda()
+        p.gate = torch.where(at, torch.tensor(values, device="cuda").bfloat16()[which], p.gate)
+        want = plain.double() * torch.sigmoid(p.gate.double())
+        bad = torch.isnan(p.gate)
+        assert bad.any() and torch.equal(torch.isnan(want), bad)
+        for dtype in (torch.float32, torch.bfloat16):
+            out, _, ws = p.attend(out_dtype=dtype)
+            assert status_of(ws) == 0
+            assert torch.equal(torch.isnan(out), bad)
+            half = 2.0 ** -16 + (U8 if dtype is torch.bfloat16 else 0)
+            off = (out.double() - want).abs() - half * want.abs() - 2.0 ** -125 * plain.double().abs()
+            if dtype is torch.bfloat16:
+                off = off - 2.0 ** -134
+            assert (off[~bad] <= 0).all(), (dtype, float(off[~bad].max()))
