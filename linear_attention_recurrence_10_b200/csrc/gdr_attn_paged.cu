@@ -32,11 +32,12 @@
 // products are 2048 and the rest the round from S through the softmax back to P V.
 //
 // A code cache is multiplied as it is, in e4m3, at twice bf16's rate and with
-// nothing to convert: the other operand is split in two e4m3 parts, x ~ hi + lo,
+// nothing to convert: the other operand is split in two 8-bit parts, x ~ hi + lo,
 // which hold 8 significant bits as bf16 does.  Q (bf16) times a power of two
-// per row splits exactly but for values 2^-17 below the row's largest.  The
+// per row, in e4m3 and e4m3, is exact for values within 2^-9 of the row's largest; smaller
+// ones are off by up to 2^-17 of the largest.  The
 // key scales multiply the scores.  The value scales sv_j enter the
-// weights, w_j = 2^(a_j + log2 sv_j - m), which P holds, with the maximum taken
+// weights, w_j = 2^(a_j + log2 sv_j - m), which P holds in e4m3 and e5m2, with the maximum taken
 // over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Two more warps split
 // Q and prepare the scales.
 //
@@ -424,8 +425,9 @@ __device__ __forceinline__ void gate2(float &a, float &b, uint32_t gates, float 
                           make_float2(1.f, 1.f));
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-    r *= inv;
-    const float2 y = mul2(make_float2(a, b), mul2(make_float2(d.y, d.x), make_float2(r, r)));
+    // (r times inv could underflow.)
+    const float2 y = mul2(mul2(make_float2(a, b), make_float2(inv, inv)),
+                          mul2(make_float2(d.y, d.x), make_float2(r, r)));
     a = y.x;
     b = y.y;
 }
@@ -435,11 +437,14 @@ __device__ __forceinline__ float gate_any(float a, float g) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_fast(g * -1.4426950408889634f)));
     return a * r;
 }
-// Four weights as e4m3 codes in two parts, with integer instructions: the conversions
-// run at 16 lanes a clock for the SM, like the exponentials beside them.  The weights come
-// times 2^-8, below 2: there f16 has e4m3's exponents (2^-14 its smallest normal value,
-// where the codes' is 2^-6), so a code is an f16 value rounded to 3 bits of mantissa,
-// without its sign's neighbour bit, which is 0.
+// Four weights in two 8-bit parts, e4m3 and what that leaves in e5m2, with integer
+// instructions: the conversions run at 16 lanes a clock for the SM, like the exponentials
+// beside them.  The weights come times 2^-8, below 2: there f16 has e4m3's exponents (2^-14
+// its smallest normal value, where the codes' is 2^-6), so a code is an f16 value rounded to
+// 3 bits of mantissa, without its sign's neighbour bit, which is 0.  The rest is at most a
+// 16th of the weight (or 2^-10); times 2^8 its f16 value rounded to 2 bits of mantissa is its
+// e5m2 code.  Together they are within 2^-8 of the weight, as bf16 is, and within 2^-14
+// below 2^-6, where a second part in e4m3, whose smallest step is 2^-9, is within 2^-10.
 __device__ __forceinline__ void split4(float a, float b, float c, float d, uint32_t &hi, uint32_t &lo) {
     const uint32_t y[2] = {f16x2(a, b), f16x2(c, d)};
     uint32_t h[2], l[2];
@@ -448,9 +453,9 @@ __device__ __forceinline__ void split4(float a, float b, float c, float d, uint3
         const uint32_t t = y[i] + 0x00400040u;  // weights are positive: round by a carry
         uint32_t rest;
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(y[i]), "r"(t & 0xff80ff80u));
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(rest), "r"(0x5c005c00u));  // 2^8; exact
         h[i] = t << 1;
-        // Rounded away from zero, whatever the sign, and shifted past it.
-        l[i] = ((rest * 2 + 0x00800080u) & 0x7fff7fffu) | (rest & 0x80008000u);
+        l[i] = rest + 0x00800080u;  // rounded away from zero, whatever the sign
     }
     hi = __byte_perm(h[0], h[1], 0x7531);
     lo = __byte_perm(l[0], l[1], 0x7531);
@@ -740,6 +745,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             constexpr int M = PAIR ? 256 : 128;
             constexpr uint32_t ID_S = instr_desc<KIND>(M, KEYS, false, false);
             constexpr uint32_t ID_O = instr_desc<KIND>(M, E4M3 ? 128 : 256, false, true);
+            constexpr uint32_t ID_O_LO = ID_O | E5M2_A;  // codes: the weights' second parts
             constexpr int STEP = E4M3 ? 32 : 16;  // keys per instruction of P V
             const uint64_t dq = smem_desc_sw128(sq, 16, 1024);
             const uint64_t dk = smem_desc_sw128(ring, 16, 1024);
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                         const int part = x >> 2, k = x & 3;
                         if (k < steps)
                             mma_ta_e4m3(tm + TM_O + 128 * h, pt + 32 * k + 8 * part,
-                                        b + k * (4096 >> 4), ID_O, x ? 1u : more);
+                                        b + k * (4096 >> 4), part ? ID_O_LO : ID_O, x ? 1u : more);
                     }
                 }
             };
@@ -934,14 +940,25 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         // and COLS of O's columns.  They agree on a row's maximum through red[], and
         // to stop, at the same barrier.
         //
-        // The reference maximum only moves when a tile's maximum passes it by
+        // The reference maximum moves up when a tile's maximum passes it by
         // more than kLazy (log2): then O and the sum are rescaled, which needs
         // the tile before's product finished.  bf16 holds a weight of any size
-        // alike; the e4m3 parts hold 2^-9 .. 448, so there the weights sit 2^6 up
+        // alike; the codes' parts hold at most 448, so there the weights sit 2^6 up
         // and may grow by 2^2.
+        //
+        // Codes: below 2^-6 a weight is off by up to 2^-14, 2^-20 of the reference.  Where one
+        // key's weight is far above the many that follow, that would add up, so there the
+        // reference also moves down, to a tile's maximum 2^kSink below it (and no more than
+        // 2^kFall below the highest: such weights are nothing beside what is summed, and the
+        // sums would overflow).  A tile's reference is then at most 2^5 times its largest
+        // weight, and all these errors add up to at most 2^7 2^-20 2^5 = 2^-8 of the sum of
+        // the weights, times the largest code, whatever the number of keys.  Scores of
+        // random rows of size 1 hardly ever move it: 64 x 4096 80 us, as without; of size 3, 89
+        // for 85.  (To the maximum of the last 8 tiles, every 8, 1 below: 85 and 89.)
         constexpr float kLazy = E4M3 ? 2.f : 8.f;
         constexpr float kUp = E4M3 ? 6.f : 0.f;
         constexpr float kShift = E4M3 ? 8.f : 0.f;  // split4 takes weights times 2^-8
+        constexpr float kSink = 5.f, kFall = 40.f;
         constexpr int KPT = KEYS / PARTS, COLS = D / PARTS, NG = 32 * PARTS;
         const int part = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t lane_off = (uint32_t)(32 * quad) << 16;
@@ -984,6 +1001,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(g + x));
             }
             float m_ref = -INFINITY, l = 0.f;
+            float lowest = -INFINITY;  // codes: how far the reference may go down
             float row_factor = 1.f;
             for (int i = 0; i < n; ++i) {
                 const int j = jt + i, k0 = (it.a + i) * KEYS;
@@ -1082,9 +1100,18 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     for (int x = 0; x < PARTS; ++x)
                         top = fmaxf(top, red[((j & 1) * PARTS + x) * 32]);
                     const bool first = m_ref == -INFINITY;
-                    const bool moves = mine && !first && top > m_ref + kLazy;
-                    const float alpha = moves ? exp2_fast(m_ref - top) : 1.f;
-                    if (first || moves) m_ref = top;
+                    bool moves = mine && !first && top > m_ref + kLazy;
+                    float to = top;
+                    if constexpr (E4M3) {
+                        lowest = fmaxf(lowest, m_ref - kFall);
+                        const float down = fmaxf(top, lowest);
+                        if (mine && down < m_ref - kSink) {
+                            moves = true;
+                            to = down;
+                        }
+                    }
+                    const float alpha = moves ? exp2_fast(m_ref - to) : 1.f;
+                    if (first || moves) m_ref = to;
                     l *= alpha;
                     const bool rescale = __any_sync(kFullMask, moves) && i > 0;
                     // -inf (nothing attended yet) as 0: every exponent below is -inf then.

@@ -82,6 +82,9 @@ __device__ __forceinline__ void mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b
             "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
+// Added to the descriptor of kind::f8f6f4: A in e5m2 (format 1; A and B choose theirs by themselves).
+constexpr uint32_t E5M2_A = 1u << 7;
+
 // D[tmem] (+)= A[tmem] * B[smem] (kind::f16): A is M rows in M TMEM lanes, its
 // K values packed two bf16 per 32-bit column (even K in the low half), so one
 // instruction (K = 16) reads 8 columns from a_tmem.
@@ -93,7 +96,7 @@ __device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
-// The same with e4m3 operands (kind::f8f6f4): four values per 32-bit column, so
+// The same with 8-bit operands (kind::f8f6f4): four values per 32-bit column, so
 // one instruction (K = 32) reads 8 columns from a_tmem.
 __device__ __forceinline__ void mma_ta_e4m3(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {

@@ -1,5 +1,7 @@
 """Edges of the paged cache's operators (gdr_kv_append, gdr_kv_gather, gdr_attn_paged) against
 their formulas in 64 bits; bounds in paged_testutil where a test states no other."""
+import math
+
 import pytest
 import torch
 
@@ -135,3 +137,121 @@ def test_gates_of_any_value(kind, new, past):
             if dtype is torch.bfloat16:
                 off = off - 2.0 ** -134
             assert (off[~bad] <= 0).all(), (dtype, float(off[~bad].max()))
+
+
+# ------------------------------------- weights far below the largest, over codes
+
+
+def shaped_codes(bits, v, H_q, H_kv, new, n_seq, seed):
+    """n_seq sequences over the same pages of codes: token j's score is about bits[j, h] (log2) for
+    kv head h, its value v[j, h].  The last `new` tokens of each are its new ones."""
+    n = bits.shape[0]
+    p = Problem(new=[1], past=[0], H_q=H_q, H_kv=H_kv, page=128, kind="e4m3", seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(n_seq * new, H_q, D, generator=g)
+    k = 0.15 * torch.randn(n, H_kv, D, generator=g)  # scores of about 0.2 besides
+    q[..., 0], k[..., 0] = 32.0, bits * (math.log(2) * D ** 0.5 / 32.0)
+    n_pages = -(-n // 128)
+    order = torch.randperm(n_pages, generator=g)
+
+    def quantised(x):
+        x = torch.cat([x, x.new_full((n_pages * 128 - n, H_kv, D), NAN)])
+        x = x.view(n_pages, 128, H_kv, D).transpose(1, 2)[order.argsort()].contiguous().cuda()
+        scale = (x.abs().amax(-1) / 448).clamp_min(2.0 ** -40)
+        return (x / scale[..., None]).to(torch.float8_e4m3fn), scale
+
+    p.k_pages, p.k_scale = quantised(k)
+    p.v_pages, p.v_scale = quantised(v)
+    p.q = q.bfloat16().cuda()
+    p.gate = torch.full_like(p.q, -41.5)
+    p.table = order.to(torch.int32).repeat(n_seq, 1).cuda().contiguous()
+    p.new, p.past, p.len = [new] * n_seq, [n - new] * n_seq, [n] * n_seq
+    p.n_seq, p.rows, p.n_tok, p.n_pages, p.width = n_seq, n_seq * new, n_seq * new, n_pages, n_pages
+    p.cu = (torch.arange(n_seq + 1) * new).to(torch.int32).cuda()
+    p.cache_len = torch.full((n_seq,), n - new, dtype=torch.int32, device="cuda")
+    return p
+
+
+def check_codes(p, out, lse, tag):
+    """Against the formula, with a bound that does not grow with the number of keys.
+
+    A weight is off by (u8 + 2^-11) of itself or by 2^-14 + 2^-17 < 2^-13.8 where it is below 2^-6,
+    at a scale where the reference is 2^6: 2^-19.8 of the reference, which is at most 2^5 times
+    the largest weight of the tile of 128 keys, or 2^-40 times the row's largest of all.  d, as
+    elsewhere, is the scores' error: fp32 sums, and Q's parts, off by 2^-17 of the row's largest
+    value each."""
+    n, rows = p.len[0], p.rows
+    k, _ = p.cached("k", 0)
+    v, vs = p.cached("v", 0)
+    q = p.q.double().unflatten(1, (p.H_kv, -1))
+    last = p.past[0] + torch.arange(rows, device="cuda") % p.new[0]
+    at_tile = torch.arange(n, device="cuda") // 128
+    n_tile = int(at_tile[-1]) + 1
+    worst = 0.0
+    for h in range(p.H_kv):
+        for r in range(q.shape[2]):
+            x = q[:, h, r]
+            off = torch.arange(n, device="cuda") > last[:, None]
+            a = (x @ k[:, h].t() * D ** -0.5).masked_fill(off, -math.inf)
+            ref_lse = torch.logsumexp(a, -1)
+            P = torch.exp(a - ref_lse[:, None])
+            y = P @ v[:, h]
+            # (a score far below the row's largest does not matter: bounded by those that weigh)
+            heavy = P > 2.0 ** -40
+            d = (x.abs() @ k[:, h].abs().t() * 256 * 2.0 ** -24
+                 + x.abs().amax(-1, keepdim=True) * 2.0 ** -17 * k[:, h].abs().sum(-1)) * D ** -0.5
+            d = torch.where(heavy, d, 0).amax(-1, keepdim=True)
+            W = P * vs[:, h]
+            top = torch.zeros(rows, n_tile, dtype=torch.float64, device="cuda").scatter_reduce(
+                1, at_tile.expand(rows, -1), W, "amax") + 2.0 ** -45 * W.amax(-1, keepdim=True)
+            codes = torch.zeros(n_tile, D, dtype=torch.float64, device="cuda").index_add(
+                0, at_tile, (v[:, h] / vs[:, h, None]).abs())
+            tol = (U8 + 2.0 ** -11 + 2 * d + 2.0 ** -19) * (P @ v[:, h].abs()) + 2.0 ** -14.8 * (top @ codes)
+            head = h * q.shape[2] + r
+            err = (out[:, head].double() - y).abs()
+            assert (err <= tol).all(), (tag, head, float((err / tol).max()))
+            e = (lse[:, head].double() - ref_lse).abs()
+            assert (e <= d[:, 0] + 2.0 ** -19 + 2.0 ** -21 * ref_lse.abs()).all(), (tag, head, float(e.max()))
+            worst = max(worst, float(err.norm() / y.norm()))
+    # the weights' roundings are independent: u8 / sqrt(3), as elsewhere; 20 rows estimate it within 1.25
+    assert worst <= 1.25 * U8 / math.sqrt(3), (tag, worst)
+
+
+@pytest.mark.parametrize("layout", [(8, 8, 1, 20), (16, 2, 200, 1)])
+@pytest.mark.parametrize("shape", ["first key", "first value", "first tile", "falling", "steps"])
+def test_codes_keep_weights_far_below_the_largest(shape, layout):
+    """Long caches of codes in which the weights' sizes change along the sequence, with values
+    whose mean is not zero, so that what is lost shows: one dominant key and many keys of a 2^8th to
+    a 2^20th of its weight; a value row of another size; scores that fall, or go up and down."""
+    H_q, H_kv, new, n_seq = layout
+    n = 32768 if new == 1 else 20001
+    g = torch.Generator().manual_seed(431)
+    j = torch.arange(n)[:, None]
+    step = (torch.tensor([8.0, 11.0, 13.0, 14.0, 15.0, 16.0, 17.0, 20.0]) if H_kv == 8 else
+            torch.tensor([13.0, 16.0]))
+    v = 1 + 0.5 * torch.randn(n, H_kv, D, generator=g)
+    if shape == "first key":
+        bits = torch.where(j == 0, step, 0.0)
+        v[0] = -v[0]
+    elif shape == "first value":
+        bits = torch.where(j == 0, step - 10, 0.0)
+        v[0] *= -1024
+    elif shape == "first tile":
+        bits = torch.where(j < 100, step - 3, 0.0)
+        v[:100] *= -1
+    elif shape == "falling":
+        bits = step * (1 - 2.5 * j / n)
+        v[: n // 3] *= -1
+    else:
+        bits = torch.where((j // 700) % 2 == 0, step * 0.75, 0.0) + 4 * torch.sin(j / 3000.0)
+        v = torch.where(((j // 700) % 2 == 0)[..., None], v, -2 * v)
+    p = shaped_codes(bits, v, H_q, H_kv, new, n_seq, seed=430)
+    out, lse, ws = p.attend(gate=False, out_dtype=torch.float32)
+    assert status_of(ws) == 0
+    check_codes(p, out, lse, shape)
+    again, _, _ = p.attend(gate=False, out_dtype=torch.float32)
+    assert torch.equal(out, again)
+    # Gates of -41.5: what is left of 2^-60 keeps its relative precision (bound: test_gates_of_any_value).
+    small, _, _ = p.attend(out_dtype=torch.float32)
+    want = out.double() * torch.sigmoid(p.gate.double())
+    assert ((small.double() - want).abs() <= 2.0 ** -16 * want.abs()).all()
