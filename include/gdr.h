@@ -452,9 +452,9 @@ gdr_status gdr_attn_decode_step(const gdr_attn_decode_args *args, void *workspac
  * Nothing about the lengths is read on the host, so a captured graph may be
  * replayed with other lengths in the same arrays.  What only the device can
  * see is checked there: a page outside [0, n_pages), a token past table_width
- * pages, a negative length, one of 2^31 - 256 tokens or more.  Such a token is not written (gdr_kv_append) or
- * leaves its output row unspecified (gdr_kv_gather, and gdr_attn_paged for
- * every row of its sequence); nothing outside the buffers is read or written,
+ * pages, a negative length, one of 2^31 - 256 tokens or more (a token that would make it that
+ * long).  Such a token is not written (gdr_kv_append) or leaves its output row unspecified
+ * (gdr_kv_gather, and gdr_attn_paged for every row of its sequence); nothing outside the buffers is read or written,
  * and the call's status word is set to GDR_ERR_INVALID_ARG.
  * Two sequences may share pages that neither writes.
  * ------------------------------------------------------------------------ */

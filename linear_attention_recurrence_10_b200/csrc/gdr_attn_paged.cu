@@ -178,7 +178,7 @@ struct Seq {
         start = (int64_t)q * p.n_rep <= FEW_ROWS ? COST_FEW : COST_MANY;
         len = before;
         const int64_t total = (int64_t)len + q;
-        if (len < 0 || total > ((int64_t)p.a.pages.table_width << p.shift) || total > 0x7fffff00LL) len = -1;
+        if (len < 0 || total > ((int64_t)p.a.pages.table_width << p.shift) || total >= kTooLong) len = -1;
     }
     __device__ __forceinline__ void load(const AttnParams &p, int s) {
         const int32_t *cu = p.a.pages.cu_seqlens + s;

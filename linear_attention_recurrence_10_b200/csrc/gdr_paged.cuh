@@ -10,6 +10,7 @@ namespace paged {
 
 constexpr int D = 256;
 constexpr int kBadPage = GDR_ERR_INVALID_ARG;
+constexpr int64_t kTooLong = 0x7fffff00;  // 2^31 - 256: no sequence has so many tokens
 constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40: a row of zeros keeps a usable scale
 
 // The sequence that owns packed row t: the s with cu[s] <= t < cu[s + 1], or n_seq
@@ -36,7 +37,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int n_seq, int t
 // rows of the cache, or -1 when the token has no valid page.
 __device__ __forceinline__ int cache_row(const gdr_kv_pages &c, int shift, int s, int g, int64_t t) {
     const int64_t i = t >> shift;
-    if (t < 0 || i >= c.table_width) return -1;
+    if (t < 0 || t + 1 >= kTooLong || i >= c.table_width) return -1;
     const int page = __ldg(c.page_table + s * c.table_stride + i);
     if (page < 0 || page >= c.n_pages) return -1;
     return (page * c.H_kv + g) * c.page_size + (int)(t & (c.page_size - 1));

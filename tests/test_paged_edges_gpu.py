@@ -255,3 +255,39 @@ def test_codes_keep_weights_far_below_the_largest(shape, layout):
     small, _, _ = p.attend(out_dtype=torch.float32)
     want = out.double() * torch.sigmoid(p.gate.double())
     assert ((small.double() - want).abs() <= 2.0 ** -16 * want.abs()).all()
+
+
+# ---------------------------------------------------------- the longest sequences
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_longest_sequence(kind):
+    """A sequence has fewer than 2^31 - 256 tokens: the last one that may be is written, read back
+    and rotated, the next is refused by every call, although the table has a page for it."""
+    p = Problem(new=[2], past=[0], page=1024, kind=kind, seed=440)
+    last = (1 << 31) - 258  # its position
+    table = torch.full((1, 1 << 21), -1, dtype=torch.int32, device="cuda")
+    table[0, last // 1024] = p.table[0, 0]
+    p.table, p.cache_len = table, torch.tensor([last], dtype=torch.int32, device="cuda")
+    before = p.k_pages.clone(), p.v_pages.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = p.append(status=status)
+    assert int(status) == 1
+    want, slack = rope64(p.q[:1], torch.tensor([last], device="cuda"), 64, 1e7)
+    assert ((q_out[:1].double() - want).abs() <= U8 * want.abs() * (1 + U8) + slack).all()
+    page, row = int(table[0, last // 1024]), last % 1024
+    for now, old in zip((p.k_pages, p.v_pages), before):
+        changed = (now.view(torch.uint8) != old.view(torch.uint8)).flatten(3).any(-1).nonzero()
+        assert changed.cpu().tolist() == [[page, 0, row], [page, 1, row]]
+    v = torch.full((2, 2, D), NAN, device="cuda")
+    status.zero_()
+    gdr.kv_gather(*p.pages, None, v, **p.scales, first=p.cache_len, status=status)
+    assert int(status) == 1
+    half = 2.0 ** -4 * 1.01 if kind == "e4m3" else 0.0
+    top = p.v[0].double().abs().amax(-1, keepdim=True)
+    assert ((v[0].double() - p.v[0].double()).abs() <= half * p.v[0].double().abs() +
+            (2.0 ** -18 * top if kind == "e4m3" else 0)).all()
+    p.cache_len += 1
+    p.cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    out, lse, ws = p.attend()
+    assert status_of(ws) == 1
