@@ -7,6 +7,7 @@ import torch
 
 import linear_attention_recurrence_10_b200 as gdr
 from paged_testutil import D, NAN, U8, Problem, rope64, status_of
+from test_paged_gpu import check_append, snapshot
 
 pytestmark = pytest.mark.gpu
 
@@ -291,3 +292,168 @@ def test_longest_sequence(kind):
     p.cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     out, lse, ws = p.attend()
     assert status_of(ws) == 1
+
+
+# ------------------------------------------------- prompts, and long read-backs
+
+
+def many(n, seed):
+    """Lengths that sum to about n: many empty sequences and of one token, some of tens, a few
+    of hundreds, in any order."""
+    g = torch.Generator().manual_seed(seed)
+    out = []
+    while sum(out) < n:
+        most = [0, 1, 1, 9, 40, 400][int(torch.randint(0, 6, (1,), generator=g))]
+        out.append(int(torch.randint(0, most + 1, (1,), generator=g)))
+    out[-1] -= sum(out) - n
+    return out
+
+
+def pasts(count, seed):
+    g = torch.Generator().manual_seed(seed + 1)
+    return torch.randint(0, 60, (count,), generator=g).tolist()
+
+
+LONG = [(593, (16, 2), 64, 64), (601, (8, 8), 16, 30), (3001, (16, 2), 32, 64), (2999, (3, 1), 128, 30),
+        (4096, (8, 8), 256, 256), (1237, (128, 1), 16, 64)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,heads,page,rot_dim", LONG)
+def test_append_prompts(n, heads, page, rot_dim, kind):
+    """More packed rows than blocks take one by one: blocks of several tokens, whose sequences
+    begin, end and are empty inside a block, and a last block that is not full."""
+    new = many(n, n)
+    p = Problem(new=new, past=pasts(len(new), n), H_q=heads[0], H_kv=heads[1], page=page, kind=kind, seed=n,
+                tail=n % 7)
+    before = snapshot(p)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = p.append(rot_dim=rot_dim, status=status)
+    assert int(status) == 0
+    check_append(p, q_out, before, rot_dim)
+    after = snapshot(p)
+    # in place and without queries: the same rows
+    for name, t in before.items():
+        getattr(p, name).copy_(t)
+    q = p.q.clone()
+    assert p.append(q=q, q_out=q, rot_dim=rot_dim) is q
+    assert torch.equal(q[:n], q_out[:n]) and torch.equal(q[n:], p.q[n:])
+    for name, t in after.items():
+        assert torch.equal(getattr(p, name).view(torch.uint8), t.view(torch.uint8)), name
+        getattr(p, name).copy_(before[name])
+    gdr.kv_append(p.k, p.v, p.k_pages, p.v_pages, p.table, p.cu, p.cache_len, rot_dim=rot_dim, **p.scales)
+    for name, t in after.items():
+        assert torch.equal(getattr(p, name).view(torch.uint8), t.view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_append_prompts_with_bad_pages(kind):
+    """Bad pages and lengths inside blocks of several tokens: the tokens around them are written."""
+    p = Problem(new=[700, 5, 800, 0, 90], past=[3, 0, 0, 4, 1], page=16, kind=kind, seed=450)
+    before = snapshot(p)
+    good = p.table.clone()
+    bad = [(0, 7), (2, 20), (2, 21)]
+    for s, i in bad:
+        p.table[s, i] = [-1, p.n_pages, 1 << 30][i % 3]
+    p.cache_len[1] = -3
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = p.append(status=status)
+    assert int(status) == 1
+    # what was not written is put there by hand, and the rest has to be right
+    want = Problem(new=p.new, past=p.past, page=16, kind=kind, seed=450)
+    want.append()
+    p.table, p.cache_len = good, want.cache_len
+    lost = torch.zeros(p.n_pages, 16, dtype=torch.bool, device="cuda")
+    for s, i in bad:
+        lost[good[s, i].long()] = True
+    lost[good[1, 0].long(), :5] = True
+    for name, old in before.items():
+        bits = torch.int32 if name.endswith("scale") else torch.uint8
+        now, ref, old = (t.view(bits) for t in (getattr(p, name), getattr(want, name), old))
+        at = lost[:, None].expand(now.shape[:3])
+        assert torch.equal(now[at], old[at]), name
+        now[at] = ref[at]
+    q_out[700:705] = rope64(p.q[700:705], torch.arange(5, device="cuda"), 64, 1e7)[0].bfloat16()
+    check_append(p, q_out, before)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,heads,page,_", LONG)
+def test_gather_many(n, heads, page, _, dtype, kind):
+    """More packed rows than blocks take one by one, from the middle of sequences, both sides and
+    one, into rows of a wider tensor."""
+    past = [m + 70 for m in many(n, n + 1)]
+    p = Problem(new=[0] * len(past), past=past, H_q=heads[0], H_kv=heads[1], page=page, kind=kind, seed=n + 2)
+    take = [m - 70 for m in past]
+    first = pasts(len(past), n + 3)
+    cu = torch.tensor([0] + take).cumsum(0).to(torch.int32).cuda()
+    begin = torch.tensor(first, dtype=torch.int32, device="cuda")
+    want = [torch.cat([p.cached(name, s)[0][f:f + t] for s, (f, t) in enumerate(zip(first, take))]).float().to(dtype)
+            for name in "kv"]
+    wide = torch.full((n + 5, 2 * heads[1] + 1, D), NAN, dtype=dtype, device="cuda")
+    k, v = wide[:, :heads[1]], wide[:, heads[1]:2 * heads[1]]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdr.kv_gather(*p.pages[:3], cu, k, v, **p.scales, first=begin, status=status)
+    assert int(status) == 0
+    assert torch.equal(k[:n], want[0]) and torch.equal(v[:n], want[1])
+    assert torch.isnan(wide[n:]).all() and torch.isnan(wide[:, -1]).all()
+    for side in range(2):
+        one = torch.full((n + 5, heads[1], D), NAN, dtype=dtype, device="cuda")
+        gdr.kv_gather(*p.pages[:3], cu, *((one, None) if side == 0 else (None, one)), **p.scales, first=begin)
+        assert torch.equal(one[:n], want[side]) and torch.isnan(one[n:]).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_gather_many_with_bad_pages(kind):
+    p = Problem(new=[0, 0, 0], past=[900, 30, 700], page=16, kind=kind, seed=460)
+    good = p.table.clone()
+    want = [torch.cat([p.cached(name, s)[0] for s in range(3)]).bfloat16() for name in "kv"]
+    p.table[0, 9], p.table[2, 33] = -5, p.n_pages
+    cu = torch.tensor([0, 900, 930, 1630], dtype=torch.int32, device="cuda")
+    out = [torch.full((1630, 2, D), NAN, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdr.kv_gather(*p.pages[:3], cu, *out, **p.scales, status=status)
+    assert int(status) == 1 and not torch.equal(p.table, good)
+    keep = torch.ones(1630, dtype=torch.bool, device="cuda")
+    keep[9 * 16:10 * 16] = False
+    keep[930 + 33 * 16:930 + 34 * 16] = False
+    for got, ref in zip(out, want):
+        assert torch.equal(got[keep], ref[keep])
+
+
+def test_append_and_gather_many_on_a_captured_stream():
+    """A prompt's append and the read-back captured once, replayed with other lengths."""
+    sizes = [[700, 300, 0], [0, 1, 900], [333, 333, 334]]
+    p = Problem(new=sizes[0], past=[0, 50, 7], page=64, kind="e4m3", seed=470, width=20, spare=30)
+    q_out = torch.empty_like(p.q)
+    k, v = (torch.empty(1000, 2, D, device="cuda") for _ in "kv")
+    calls = lambda: (gdr.kv_append(p.k, p.v, p.k_pages, p.v_pages, p.table, p.cu, p.cache_len, q=p.q, q_out=q_out,
+                                   **p.scales),
+                     gdr.kv_gather(*p.pages, k, v, first=p.cache_len, **p.scales))
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for i, new in enumerate(sizes):
+        x = Problem(new=new, past=[0, 50, 7], page=64, kind="e4m3", seed=471 + i, width=20,
+                    tail=1000 - sum(new))
+        assert x.n_pages <= p.n_pages
+        for name in ("q", "k", "v", "table", "cu", "cache_len"):
+            getattr(p, name).copy_(getattr(x, name))
+        for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+            getattr(p, name)[:x.n_pages].copy_(getattr(x, name))
+        before = snapshot(x)
+        for t in (q_out, k, v):
+            t.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in before:
+            setattr(x, name, getattr(p, name)[:x.n_pages].clone())
+        check_append(x, q_out, before)
+        n = sum(new)
+        for name, got in (("k", k), ("v", v)):
+            want = torch.cat([x.cached(name, s)[0][x.past[s]:] for s in range(3)])
+            assert torch.equal(got[:n], want.float()) and torch.isnan(got[n:]).all()
+    del graph
