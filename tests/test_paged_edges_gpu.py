@@ -457,3 +457,21 @@ def test_append_and_gather_many_on_a_captured_stream():
             want = torch.cat([x.cached(name, s)[0][x.past[s]:] for s in range(3)])
             assert torch.equal(got[:n], want.float()) and torch.isnan(got[n:]).all()
     del graph
+
+
+@pytest.mark.parametrize("times", [16, 1024])
+def test_codes_queries_with_an_outlying_value(times):
+    """Over codes a query's values are held to 2^-17 of the row's largest: one value `times` the
+    others', where the keys have nothing or little, leaves the others coarser (d in check_codes)."""
+    n = 3000
+    g = torch.Generator().manual_seed(480)
+    v = 1 + 0.5 * torch.randn(n, 2, D, generator=g)
+    p = shaped_codes(torch.zeros(n, 2), v, 16, 2, 40, 1, seed=481)
+    p.q[..., 0] = 0
+    p.q[..., 77] = 3.0 * times
+    codes = p.k_pages.view(torch.uint8)
+    codes[..., 77] = 0
+    codes[:, :, ::5, 77] = torch.tensor(1024.0 / times).clamp_max(64).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    out, lse, ws = p.attend(gate=False, out_dtype=torch.float32)
+    assert status_of(ws) == 0
+    check_codes(p, out, lse, times)
