@@ -28,7 +28,7 @@
 // 128 KB tile of keys and values for 16.8 MFLOP, and the L2 cache cannot feed 148 of
 // them (2970 clocks a tile, a third of them waiting for loads).  The two CTAs of a cluster
 // take 256 rows and load half of every tile each (cta_group::2 multiplies both halves
-// for both): no wait for loads is left, and a tile takes 2500 clocks, of which the
+// for both): the waits for loads are short, and a tile takes 2700 clocks, of which the
 // products are 2048 and the rest the round from S through the softmax back to P V.
 //
 // A code cache is multiplied as it is, in e4m3, at twice bf16's rate and with
@@ -41,16 +41,21 @@
 // over a_j + log2 sv_j; the softmax's sum is that of w_j / sv_j.  Two more warps split
 // Q and prepare the scales.
 //
-// What bounds it, 16 query heads over 2 key/value heads:
-//   decode, 64 sequences of 4096 tokens: bf16, 107 us, the 0.54 GB of the cache at 5.0 TB/s;
-//     codes, 90 us (0.27 GB, 3.0 TB/s): the products, 3100 clocks a tile with operands from shared
-//     memory, 128 rows of which 8 are wanted, against 2800 for a tile's bytes.  Spreading those
-//     8 rows' softmax over all warps brought nothing.
-//   2048 tokens after 6144, bf16: 228 us, 1.06 PFLOP/s with clocks near 1.5 GHz under the
-//     power limit (200 us, 1.2 PFLOP/s, alone on a cool card).
-//   4 prompts of 4096, bf16: 565 us, 0.97 PFLOP/s; of that the output gates are 85 us: an
-//     exponential and half a reciprocal a value, while nothing is multiplied.
-//   the same by codes: the softmax of a tile, 3900 clocks, four threads a row and three
+// What bounds it, 16 query heads over 2 key/value heads (clocks by stamps in the kernel, which
+// add some per cent):
+//   decode, 64 sequences of 4096 tokens: bf16, 106 us, the 0.54 GB of the cache at 5.1 TB/s;
+//     codes, 89 us (0.27 GB, 3.1 TB/s): no unit is full (tensor pipe 44%, issue slots 28%).  Of
+//     4200 clocks a tile the softmax's warps take 3550 from scores to weights, for which the
+//     issuing thread waits 1250; one warp a scheduler has rows, 8 of its 32, so that is one
+//     warp's latency.  The products are 2050, of 128 rows.  Spreading those 8 rows' softmax over
+//     all warps was no faster.
+//   2048 tokens after 6144, bf16: 225 us, 1.06 PFLOP/s with clocks near 1.5 GHz under the
+//     power limit (200 us, 1.2 PFLOP/s, alone on a cool card).  The softmax's warps wait 450
+//     clocks of a tile; their round is 2250.  Before the first tile a CTA spends 17000 clocks,
+//     most of them on its place in the batch (make_plan: a binary search in 64-bit divisions).
+//   4 prompts of 4096, bf16: 560 us, 0.98 PFLOP/s: 14.5 items a pair, whose ends, output gates
+//     most of them, take 10700 clocks each, a fifth of the time, while nothing is multiplied.
+//   chunks by codes: the softmax of a tile, 3800 clocks of 4150, four threads a row and three
 //     times bf16's instructions a key (scales, two parts).
 // P in shared memory with S two tiles ahead (pairs) measured 238 us for 232: P's one buffer
 // then makes the softmax wait for P V.
@@ -1068,8 +1073,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 dead = group_sync_or(1 + quad, NG, !ok || fault);
                 if (dead) break;
                 // The MMA takes V's keys in steps of 16 (32 codes): what pages hold between
-                // the sequence's end and the step's becomes zero.  (Here, and not just before P's
-                // arrival: 64 x 4096 over codes 89.2 instead of 91.1 us.)
+                // the sequence's end and the step's becomes zero.  (Just before P's arrival instead:
+                // 64 ragged sequences of up to 8190 tokens over codes 90.2 us for 88.6, over bf16 and
+                // shorter ones alike.)
                 const int keys = it.end - k0;
                 constexpr int STEP = E4M3 ? 32 : 16;
                 const bool clears = keys < KEYS && (keys & (STEP - 1));

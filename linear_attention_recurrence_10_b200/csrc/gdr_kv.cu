@@ -14,12 +14,13 @@
 // once, and a warp reads four rows before it writes the first.  64 sequences of 4096
 // tokens from codes (0.81 GB): 148 us, 5.5 TB/s; with one row a warp and a look-up a row, 224 us.
 //
-// append is bound by instructions, of which most are the codes' (a division a value)
-// and the queries' rotation.  The angles are taken in double, once per token for all its
+// append: the angles are taken in double, once per token for all its
 // heads.  A row's rotated dims are a quarter of it in the layers this is for, so queries go by
 // pairs of 16-byte chunks instead of rows: whole warps rotate, and the rest is copied.  Four
 // prompts of 4096 tokens, 16 query and 2 key/value heads, to codes (0.32 GB): 69 us,
-// 4.6 TB/s; by rows, 98 us.
+// 4.6 TB/s; by rows, 98 us.  To bf16 (0.34 GB, no divisions) it is 71 us.  Neither memory (70% of a
+// copy's rate) nor the issue slots (55%) are full: blocks are short, and each searches its
+// sequences and takes its pages and angles before most of its loads.
 #include <cuda_fp8.h>
 #include <math.h>
 
