@@ -959,7 +959,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         // weight, and all these errors add up to at most 2^7 2^-20 2^5 = 2^-8 of the sum of
         // the weights, times the largest code, whatever the number of keys.  Scores of
         // random rows of size 1 hardly ever move it: 64 x 4096 80 us, as without; of size 3, 89
-        // for 85.  (To the maximum of the last 8 tiles, every 8, 1 below: 85 and 89.)
+        // for 85.  (To the maximum of the last 8 tiles, every 8, 1 below: 85 and 89.)  A tile of
+        // which a row attends nothing, its last, moves it too, for nothing; to test for that costs 1%.
         constexpr float kLazy = E4M3 ? 2.f : 8.f;
         constexpr float kUp = E4M3 ? 6.f : 0.f;
         constexpr float kShift = E4M3 ? 8.f : 0.f;  // split4 takes weights times 2^-8
