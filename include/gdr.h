@@ -568,6 +568,16 @@ gdr_status gdr_attn_paged_workspace_size(const gdr_attn_paged_args *args, size_t
 gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace,
                           size_t workspace_bytes, gdr_stream_t stream);
 
+/* Diagnostic: gdr_attn_paged with its device-side waits limited to `wait_ns` nanoseconds
+ * and no query tile ever delivered, so that waits run out.  Once the work has finished
+ * the status word reads GDR_ERR_TIMEOUT, the outputs are incomplete (unspecified), and
+ * the device is left usable for the calls that follow.  Arguments and checks are those
+ * of gdr_attn_paged, with n_tok and n_seq at least 1 and wait_ns in
+ * [GDR_SELFTEST_MIN_WAIT_NS, GDR_SELFTEST_MAX_WAIT_NS] (else GDR_ERR_INVALID_ARG). */
+gdr_status gdr_attn_paged_selftest_wait_expiry(const gdr_attn_paged_args *args, void *workspace,
+                                               size_t workspace_bytes, uint64_t wait_ns,
+                                               gdr_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * The routed-expert MoE feed-forward block at decode time (the FFN of the
  * hybrid decoder's MoE models: Core AI card for Qwen3.6-35B-A3B, first

@@ -186,6 +186,8 @@ def lib(path: str = LIB_PATH) -> ctypes.CDLL:
     h.gdr_attn_paged_workspace_size.restype = ctypes.c_int
     h.gdr_attn_paged.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
     h.gdr_attn_paged.restype = ctypes.c_int
+    h.gdr_attn_paged_selftest_wait_expiry.argtypes = [_vp, _vp, ctypes.c_size_t, ctypes.c_uint64, _vp]
+    h.gdr_attn_paged_selftest_wait_expiry.restype = ctypes.c_int
     h.gdr_moe_workspace_size.argtypes = [ctypes.POINTER(MoeArgs), ctypes.POINTER(ctypes.c_size_t)]
     h.gdr_moe_workspace_size.restype = ctypes.c_int
     h.gdr_moe_decode.argtypes = [ctypes.POINTER(MoeArgs), _vp, ctypes.c_size_t, _vp]

@@ -30,7 +30,7 @@ cudaError_t launch_attn_decode_args(const gdr_attn_decode_args *a, int n_split, 
 cudaError_t launch_kv_append(const gdr_kv_append_args *a, cudaStream_t s);
 cudaError_t launch_kv_gather(const gdr_kv_gather_args *a, cudaStream_t s);
 size_t attn_paged_workspace_bytes(int n_sm);
-cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cudaStream_t s);
+cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, uint64_t wait_ns, cudaStream_t s);
 size_t moe_workspace_bytes(int n_tok, int n_exp, int top_k, int inter, int s_inter, int hidden);
 size_t moe_route_smem_bytes(int n_tok, int n_exp, int top_k);
 cudaError_t launch_moe_args(const gdr_moe_args *a, void *workspace, cudaStream_t s);
@@ -560,8 +560,11 @@ gdr_status gdr_attn_paged_workspace_size(const gdr_attn_paged_args *args, size_t
     return GDR_OK;
 }
 
-gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace, size_t ws_bytes,
-                          gdr_stream_t stream) {
+}  // extern "C"
+
+// wait_ns 0: the ordinary call; otherwise the diagnostic with that limit on its waits.
+static gdr_status attn_paged_impl(const gdr_attn_paged_args *args, void *workspace, size_t ws_bytes,
+                                  uint64_t wait_ns, gdr_stream_t stream) {
     if (!args) return GDR_ERR_INVALID_ARG;
     gdr_attn_paged_args a = *args;
     GDR_TRY(attn_paged_check(&a));
@@ -581,7 +584,21 @@ gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace, size
     if (!workspace || ws_bytes < gdr::attn_paged_workspace_bytes(device_sm_count()))
         return GDR_ERR_WORKSPACE;
     if (!aligned16(workspace)) return GDR_ERR_MISALIGNED;
-    return from_cuda(gdr::launch_attn_paged(&a, workspace, (cudaStream_t)stream));
+    return from_cuda(gdr::launch_attn_paged(&a, workspace, wait_ns, (cudaStream_t)stream));
+}
+
+extern "C" {
+
+gdr_status gdr_attn_paged(const gdr_attn_paged_args *args, void *workspace, size_t ws_bytes,
+                          gdr_stream_t stream) {
+    return attn_paged_impl(args, workspace, ws_bytes, 0, stream);
+}
+
+gdr_status gdr_attn_paged_selftest_wait_expiry(const gdr_attn_paged_args *args, void *workspace,
+                                               size_t ws_bytes, uint64_t wait_ns, gdr_stream_t stream) {
+    if (wait_ns < GDR_SELFTEST_MIN_WAIT_NS || wait_ns > GDR_SELFTEST_MAX_WAIT_NS) return GDR_ERR_INVALID_ARG;
+    if (!args || args->pages.n_seq == 0 || args->n_tok == 0) return GDR_ERR_INVALID_ARG;
+    return attn_paged_impl(args, workspace, ws_bytes, wait_ns, stream);
 }
 
 }  // extern "C"

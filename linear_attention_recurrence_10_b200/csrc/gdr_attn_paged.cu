@@ -60,7 +60,7 @@
 // P in shared memory with S two tiles ahead (pairs) measured 238 us for 232: P's one buffer
 // then makes the softmax wait for P V.
 //
-// Every wait is bounded (2 s); on expiry a role records GDR_ERR_TIMEOUT, the
+// Every wait is bounded (2 s, less in the self-test); on expiry a role records GDR_ERR_TIMEOUT, the
 // others run into their own limits, copies and commits in flight are waited
 // for (bounded), tensor memory is freed and the CTA returns.
 #include "gdr_tmap.cuh"
@@ -143,6 +143,8 @@ struct AttnParams {
     int k_rows, v_rows;  // rows of a K and V box
     int n_rows;       // rows of the cache: a row past the end reads as zeros
     float scale_log2;
+    int withhold;       // diagnostic: no Q tile is loaded, so that every wait for one runs out
+    uint64_t wait_ns;   // limit of a wait
     int *status;      // workspace
     Desc *desc;       // [CTAs]
     float *part_ml;   // [2 CTAs][128][2]: maximum (log2) and sum
@@ -340,7 +342,7 @@ __device__ void make_plan(const AttnParams &p, int n_thr, int64_t *warp_sum, Pla
 __device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, uint64_t limit) {
     return mbar_wait(bar, parity, limit);
 }
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint64_t limit = kWaitNs) {
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint64_t limit) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -354,7 +356,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, uint64_
 
 // The same by looking again and again: for a barrier at which another CTA arrives (a waiting
 // thread that the hardware has suspended is woken late by that: by up to 2000 clocks here).
-__device__ __noinline__ bool spin_on(uint64_t *bar, uint32_t parity) {
+__device__ __noinline__ bool spin_on(uint64_t *bar, uint32_t parity, uint64_t limit) {
     const uint64_t start = global_ns();
     for (uint32_t i = 1;; ++i) {
         uint32_t done;
@@ -366,7 +368,7 @@ __device__ __noinline__ bool spin_on(uint64_t *bar, uint32_t parity) {
             : "r"(smem_u32(bar)), "r"(parity)
             : "memory");
         if (done) return true;
-        if ((i & 255) == 0 && global_ns() - start > kWaitNs) return false;
+        if ((i & 255) == 0 && global_ns() - start > limit) return false;
     }
 }
 
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
     const uint32_t tm = *tmem_slot;
     auto report = [&](int status) { atomicMax(&desc->status, status); };
     auto full_wait = [&](int use) {
-        return wait_bar(full + use % NSLOT, (uint32_t)(use / NSLOT) & 1u);
+        return wait_bar(full + use % NSLOT, (uint32_t)(use / NSLOT) & 1u, p.wait_ns);
     };
     // The swizzled tiles must start on 1024-byte boundaries.
     const bool usable = (sbase & 1023u) == 0;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             // One slot: n_box rows of boxes with n_col boxes each.
             auto acquire = [&](int use) {
                 if (use >= NSLOT && lane == 0)
-                    ok = wait_bar(empty + use % NSLOT, (uint32_t)(use / NSLOT - 1) & 1u);
+                    ok = wait_bar(empty + use % NSLOT, (uint32_t)(use / NSLOT - 1) & 1u, p.wait_ns);
                 ok = __shfl_sync(kFullMask, ok, 0);
                 return ok;
             };
@@ -685,14 +687,14 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             const int n = it.b - it.a, base = n_use;
             int row = page_row(it.a), row1 = page_row(it.a + 1);
             if (n_item > 0) {
-                if (lane == 0) ok = wait_bar(q_free, (uint32_t)(n_item - 1) & 1u);
+                if (lane == 0) ok = wait_bar(q_free, (uint32_t)(n_item - 1) & 1u, p.wait_ns);
                 ok = __shfl_sync(kFullMask, ok, 0);
                 if (!ok) break;
             }
             ++n_item;
             if (lane == 0) {
                 bulk_expect(q_full, (uint32_t)(4 * 128 * p.n_rep * p.cta_tok));
-                for (int b = 0; b < 4; ++b)
+                for (int b = 0; b < 4 && !p.withhold; ++b)
                     tma_load_3d(sq + b * BOX, &p.tm_q, b * 64, it.g * p.n_rep, it.row0, q_full);
             }
             __syncwarp();
@@ -708,17 +710,16 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         bad = __any_sync(kFullMask, bad);
         if (lane == 0) {
             if (bad) report(kBadPage);
-            if (!ok) {
-                report(kTimeout);
-                // No copy may land after the CTA ends.
-                if (n_item > 0) wait_bar(q_full, (uint32_t)(n_item - 1) & 1u);
-                for (int u = max(0, n_use - NSLOT); u < n_use; ++u) full_wait(u);
-                for (int u = max(0, n_raw - NRAW); u < n_raw; ++u)
-                    wait_bar(raw_full + u % NRAW, (uint32_t)(u / NRAW) & 1u);
-            }
+            if (!ok) report(kTimeout);
+            // No copy may land after the CTA ends (where all went well, all have).
+            if (n_item > 0) wait_bar(q_full, (uint32_t)(n_item - 1) & 1u, p.wait_ns);
+            for (int u = max(0, n_use - NSLOT); u < n_use; ++u)
+                wait_bar(full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, kWaitNs);
+            for (int u = max(0, n_raw - NRAW); u < n_raw; ++u)
+                wait_bar(raw_full + u % NRAW, (uint32_t)(u / NRAW) & 1u, kWaitNs);
             // Nor may an arrival that a commit owes: the last use of every slot, the
             // last item's Q.
-            const uint64_t lim = ok ? kWaitNs : kDrainNs;
+            const uint64_t lim = ok ? p.wait_ns : kDrainNs;
             for (int u = max(0, n_use - NSLOT); u < n_use; ++u)
                 wait_bar(empty + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, lim);
             if (n_item > 0) wait_bar(q_free, (uint32_t)(n_item - 1) & 1u, lim);
@@ -735,7 +736,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 int u = 0, n_item = 0;
                 while (ok && walk.next(p, it)) {
                     if (it.n_kv == 0) continue;
-                    ok = wait_bar(q_full, (uint32_t)n_item & 1u);
+                    ok = wait_bar(q_full, (uint32_t)n_item & 1u, p.wait_ns);
                     if (ok) mbar_arrive_at(peer_q, 0);
                     for (const int end = u + 2 * (it.b - it.a); u < end && ok; ++u) {
                         ok = full_wait(u);
@@ -760,10 +761,10 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                 else commit(smem_u32(bar));
             };
             auto landed = [&](int u) {  // in both CTAs of a pair
-                return full_wait(u) && (!PAIR || spin_on(peer_full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u));
+                return full_wait(u) && (!PAIR || spin_on(peer_full + u % NSLOT, (uint32_t)(u / NSLOT) & 1u, p.wait_ns));
             };
             auto wait_both = [&](uint64_t *bar, uint32_t parity) {  // for arrivals from both CTAs of a pair
-                return PAIR ? spin_on(bar, parity) : wait_bar(bar, parity);
+                return PAIR ? spin_on(bar, parity, p.wait_ns) : wait_bar(bar, parity, p.wait_ns);
             };
             bool ok = true;
             int jt = 0, base = 0, n_item = 0;
@@ -820,8 +821,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             while (ok && walk.next(p, it)) {
                 if (it.n_kv == 0) continue;
                 const int n = it.b - it.a;
-                ok = wait_bar(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u) &&
-                     (!PAIR || spin_on(peer_q, (uint32_t)n_item & 1u)) && score(jt, base + use_k<SPT>(0));
+                ok = wait_bar(E4M3 ? q_split : q_full, (uint32_t)n_item & 1u, p.wait_ns) &&
+                     (!PAIR || spin_on(peer_q, (uint32_t)n_item & 1u, p.wait_ns)) && score(jt, base + use_k<SPT>(0));
                 if (n == 1 && ok) done(q_free);
                 for (int i = 0; i < n && ok; ++i) {
                     if (i + 1 < n) {
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         int jt = 0, n_item = 0;
         while (ok && walk.next(p, it)) {
             if (it.n_kv == 0) continue;
-            ok = __all_sync(kFullMask, wait_bar(q_full, (uint32_t)n_item & 1u));
+            ok = __all_sync(kFullMask, wait_bar(q_full, (uint32_t)n_item & 1u, p.wait_ns));
             if (!ok) break;
             // Row r: 256 bf16 values, 16-byte chunk j of box b at chunk j ^ (r % 8).  Eight lanes
             // a row, each with 16 values of either half: all of a row is read before any of
@@ -915,9 +916,9 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_split);
             for (int j = it.a; j < it.b; ++j, ++jt) {
-                ok = wait_bar(raw_full + jt % NRAW, (uint32_t)(jt / NRAW) & 1u);
+                ok = wait_bar(raw_full + jt % NRAW, (uint32_t)(jt / NRAW) & 1u, p.wait_ns);
                 // The stage was read by the softmax two tiles back.
-                if (jt >= 2) ok = ok && wait_bar(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, kWaitNs);
+                if (jt >= 2) ok = ok && wait_bar(bar_p + (jt & 1), (uint32_t)((jt - 2) >> 1) & 1u, p.wait_ns);
                 ok = __all_sync(kFullMask, ok);
                 if (!ok) break;
                 float *st = scales + (jt & 1) * 3 * KEYS;
@@ -1011,8 +1012,8 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
             float row_factor = 1.f;
             for (int i = 0; i < n; ++i) {
                 const int j = jt + i, k0 = (it.a + i) * KEYS;
-                bool ok = wait_bar(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u);
-                if (E4M3) ok = ok && wait_bar(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u);
+                bool ok = wait_bar(bar_s + (j & 1), (uint32_t)(j >> 1) & 1u, p.wait_ns);
+                if (E4M3) ok = ok && wait_bar(sc_full + (j & 1), (uint32_t)(j >> 1) & 1u, p.wait_ns);
                 ok = __all_sync(kFullMask, ok);
                 // bf16: in two chunks of the thread's keys, read twice, which is half the code
                 // of holding all of them (the roles share the instruction cache).  Codes: in one
@@ -1163,7 +1164,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     }
                     l += (l2.x + l2.y) + (l3.x + l3.y);
                     if (rescale) {
-                        fault = !__all_sync(kFullMask, wait_o(j - 1, kWaitNs)) || fault;
+                        fault = !__all_sync(kFullMask, wait_o(j - 1, p.wait_ns)) || fault;
                         if (!fault) {
                             fence_after_sync();
 #pragma unroll 1
@@ -1219,7 +1220,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
                     if (gated && has[k] && x < COLS) gates[k] = __ldg(gate_at[k] + x / 8);
             };
             fetch_gate(0);
-            const bool ok = wait_o(jt - 1, kWaitNs);
+            const bool ok = wait_o(jt - 1, p.wait_ns);
             dead = group_sync_or(1 + quad, NG, !ok || fault);
             if (dead) break;
             l = 0.f;  // in one order in all its threads
@@ -1328,7 +1329,7 @@ __global__ void __launch_bounds__(Layout<E4M3>::THREADS, 1)
         }
         if ((dead || fault) && lane == 0) report(kTimeout);
         // The product before the last is waited for by nobody: its commit must land too.
-        if (jt >= 2) wait_o(jt - 2, dead ? kDrainNs : kWaitNs);
+        if (jt >= 2) wait_o(jt - 2, dead ? kDrainNs : p.wait_ns);
         if (dead && jt >= 1) wait_o(jt - 1, kDrainNs);
     }
 
@@ -1488,7 +1489,8 @@ size_t attn_paged_workspace_bytes(int n_sm) {
     return paged::ws_o(n_sm) + (size_t)2 * n_sm * paged::ROWS * paged::D * 4;
 }
 
-cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cudaStream_t s) {
+// wait_ns 0: the ordinary limit; otherwise the diagnostic with that limit.
+cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, uint64_t wait_ns, cudaStream_t s) {
     using namespace paged;
     const gdr_kv_pages &c = a->pages;
     int dev = 0, n_sm = 0;
@@ -1515,6 +1517,8 @@ cudaError_t launch_attn_paged(const gdr_attn_paged_args *a, void *workspace, cud
     p.v_rows = c.page_size < v_keys ? c.page_size : v_keys;
     p.n_rows = c.n_pages * c.H_kv * c.page_size;
     p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+    p.withhold = wait_ns != 0;
+    p.wait_ns = wait_ns ? wait_ns : kWaitNs;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.status = reinterpret_cast<int *>(ws);
     p.desc = reinterpret_cast<Desc *>(ws + WS_DESC);

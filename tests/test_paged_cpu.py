@@ -345,3 +345,17 @@ def test_host_tensors_are_refused_where_there_is_a_gpu(monkeypatch, kind):
     for name, call in _calls(_tensors(kind)).items():
         with pytest.raises(ValueError, match=f"{name}.*CUDA device"):
             call()
+
+
+@host_only
+def test_selftest_wait_expiry_refusals(lib):
+    """The wait-expiry self-test has gdr_attn_paged's checks, a range for its limit, and no empty call."""
+    f, ws, n = lib.gdr_attn_paged_selftest_wait_expiry, FAKE + (1 << 44), ctypes.c_size_t(1 << 30)
+    a = _attn()
+    for wait_ns in (0, 99_999, 2_000_000_001):
+        assert f(ctypes.byref(a), ws, n, wait_ns, None) == INVALID
+    assert f(None, ws, n, 20_000_000, None) == INVALID
+    assert f(ctypes.byref(a), ws, 16, 20_000_000, None) == WORKSPACE
+    for kw, want in ((dict(n_tok=0), INVALID), (dict(n_seq=0), INVALID), (dict(d=128), UNSUPPORTED),
+                     (dict(q=None), INVALID), (dict(out=FAKE + 8), MISALIGNED)):
+        assert f(ctypes.byref(_attn(**kw)), ws, n, 20_000_000, None) == want, kw

@@ -1,11 +1,13 @@
 """Edges of the paged cache's operators (gdr_kv_append, gdr_kv_gather, gdr_attn_paged) against
 their formulas in 64 bits; bounds in paged_testutil where a test states no other."""
 import math
+import time
 
 import pytest
 import torch
 
 import linear_attention_recurrence_10_b200 as gdr
+from linear_attention_recurrence_10_b200 import _abi
 from paged_testutil import D, NAN, U8, Problem, rope64, status_of
 from test_paged_gpu import check_append, snapshot
 
@@ -475,3 +477,35 @@ def test_codes_queries_with_an_outlying_value(times):
     out, lse, ws = p.attend(gate=False, out_dtype=torch.float32)
     assert status_of(ws) == 0
     check_codes(p, out, lse, times)
+
+
+# ------------------------------------------------------------- waits that run out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [[1, 1, 3], [300, 400]])  # (the second by pairs of blocks, for bf16)
+def test_wait_expiry_reports_timeout_and_leaves_gpu_usable(kind, new):
+    """Every wait of the attention kernel is bounded.  The self-test runs the ordinary kernels with
+    a limit of 20 ms and no query tile ever delivered (a barrier nothing arrives at): the roles give
+    up, wait for their copies in flight, free the tensor memory and return, with the status word set.
+    An ordinary call right after, which takes all of an SM's tensor memory, is right.  With few
+    keys the loads end before the ring is full, with many they wait for it."""
+    for past in (0, 3000):
+        p = Problem(new=new, past=[past] * len(new), page=64, kind=kind, seed=490)
+        p.put_plain()
+        out, lse = torch.empty_like(p.q), torch.empty(p.rows, 16, device="cuda")
+        a = gdr._attn_paged_args(p.q, *p.pages, p.cache_len, out, p.k_scale, p.v_scale, p.gate, lse, None)
+        n = gdr.attn_paged_workspace_size(p.q, *p.pages, p.cache_len, out, **p.scales)
+        ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        start = time.perf_counter()
+        st = _abi.lib().gdr_attn_paged_selftest_wait_expiry(a, ws.data_ptr(), n, 20_000_000,
+                                                            torch.cuda.current_stream().cuda_stream)
+        assert st == 0, gdr.status_string(st)
+        torch.cuda.synchronize()
+        # At most: the ring's slots, Q twice and the last product, 20 ms each.
+        assert time.perf_counter() - start < 2.0
+        assert status_of(ws) == 6  # GDR_ERR_TIMEOUT
+        out, lse, ws = p.attend(workspace=ws)
+        assert status_of(ws) == 0
+        p.check_attend(out, lse)
