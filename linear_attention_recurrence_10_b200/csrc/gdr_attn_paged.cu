@@ -43,17 +43,17 @@
 //
 // What bounds it, 16 query heads over 2 key/value heads (clocks by stamps in the kernel, which
 // add some per cent):
-//   decode, 64 sequences of 4096 tokens: bf16, 106 us, the 0.54 GB of the cache at 5.1 TB/s;
-//     codes, 89 us (0.27 GB, 3.1 TB/s): no unit is full (tensor pipe 44%, issue slots 28%).  Of
+//   decode, 64 sequences of 4096 tokens: bf16, 107 us, the 0.54 GB of the cache at 5.0 TB/s;
+//     codes, 90 us (0.27 GB, 3.0 TB/s): no unit is full (tensor pipe 44%, issue slots 28%).  Of
 //     4200 clocks a tile the softmax's warps take 3550 from scores to weights, for which the
 //     issuing thread waits 1250; one warp a scheduler has rows, 8 of its 32, so that is one
 //     warp's latency.  The products are 2050, of 128 rows.  Spreading those 8 rows' softmax over
 //     all warps was no faster.
-//   2048 tokens after 6144, bf16: 225 us, 1.06 PFLOP/s with clocks near 1.5 GHz under the
+//   2048 tokens after 6144, bf16: 225 to 228 us, 1.06 PFLOP/s with clocks near 1.5 GHz under the
 //     power limit (200 us, 1.2 PFLOP/s, alone on a cool card).  The softmax's warps wait 450
 //     clocks of a tile; their round is 2250.  Before the first tile a CTA spends 17000 clocks,
 //     most of them on its place in the batch (make_plan: a binary search in 64-bit divisions).
-//   4 prompts of 4096, bf16: 560 us, 0.98 PFLOP/s: 14.5 items a pair, whose ends, output gates
+//   4 prompts of 4096, bf16: 560 to 567 us, 0.97 PFLOP/s: 14.5 items a pair, whose ends, output gates
 //     most of them, take 10700 clocks each, a fifth of the time, while nothing is multiplied.
 //   chunks by codes: the softmax of a tile, 3800 clocks of 4150, four threads a row and three
 //     times bf16's instructions a key (scales, two parts).
