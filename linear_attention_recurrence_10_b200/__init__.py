@@ -75,6 +75,9 @@ def _row_stride(t: torch.Tensor, what: str) -> int:
 def _stream(stream, device) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream(device)
+    # (Without a GPU the library's own checks run, and its launch fails.)
+    elif device.type != "cuda" and torch.cuda.is_available():
+        raise ValueError(f"tensors must be on a CUDA device, not {device}")
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 

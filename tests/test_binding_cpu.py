@@ -148,3 +148,41 @@ def test_every_entry_reaches_the_launch_without_a_device():
         with pytest.raises(gdr.GdrError) as e:
             call()
         assert e.value.status == 5 and name in str(e.value), (name, str(e.value))  # GDR_ERR_CUDA
+
+
+def test_host_tensors_are_refused_where_there_is_a_gpu(monkeypatch):
+    """With a stream given, tensors in host memory do not reach the library on a machine with a GPU
+    (here: a stand-in for the library, and a torch that says it has one)."""
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                assert name.endswith("workspace_size"), f"{name} was called with host addresses"
+                return 0
+            return call
+
+    bf = torch.bfloat16
+    rows = lambda n, dtype=bf: torch.zeros(n, 2, 128, dtype=dtype)
+    gates = lambda n: torch.zeros(n, 2)
+    state, cu = torch.zeros(4, 2, 128, 128), torch.tensor([0, 4], dtype=torch.int32)
+    kv = lambda: torch.zeros(3, 2, 64, 256, dtype=bf)
+    new = lambda H: torch.zeros(3, H, 256, dtype=bf)
+    calls = [
+        lambda: gdr.decode_step(rows(4), rows(4), rows(4), gates(4), gates(4), state, rows(4), stream=0),
+        lambda: gdr.decode_multi(rows(8), rows(8), rows(8), gates(8), gates(8), state, rows(8), n_tokens=2,
+                                 stream=0),
+        lambda: gdr.prefill_chunked(rows(4), rows(4), rows(4), gates(4), gates(4), cu, rows(4),
+                                    cu_seqlens_host=[0, 4], stream=0),
+        lambda: gdr.prefill_chunked_noalloc(rows(4), rows(4), rows(4), gates(4), gates(4), cu, rows(4),
+                                            cu_seqlens_host=[0, 4], stream=0),
+        lambda: gdr.rmsnorm_gated(rows(4), rows(4), rows(4), stream=0),
+        lambda: gdr.attn_decode_step(new(16), new(16), new(2), new(2), kv(), kv(),
+                                     torch.zeros(3, dtype=torch.int32), new(16), kv_bound=63, stream=0),
+        lambda: gdr.moe_decode(torch.zeros(2, 256, dtype=bf), torch.zeros(8, 256, dtype=bf),
+                               torch.zeros(8, 64, 256, dtype=bf), torch.zeros(8, 256, 32, dtype=bf),
+                               torch.zeros(2, 256), top_k=2, stream=0),
+    ]
+    monkeypatch.setattr(_abi, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    for call in calls:
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
